@@ -1,0 +1,165 @@
+// Residual addition and RMSNorm in one pass (kva_op_add_rmsnorm):
+//     h' = h + x (rounded to the stream's type),  y = h' / sqrt(mean(h'^2) + eps) * g,
+// y in 16 bits or as q8_0 blocks of 32 (int8 codes, fp16 scale max|y| / 127).
+// The norm is taken of the stored row, so a later reader of the stream finds the row that was
+// normalised.  The sum of squares is fp32.
+#include "../../include/kva_ops.h"
+#include "kva_common.cuh"
+
+namespace kva {
+namespace {
+
+template <typename T>
+struct Io;
+template <>
+struct Io<float> {
+  __device__ static __forceinline__ float4 load(const float* p) { return *reinterpret_cast<const float4*>(p); }
+  __device__ static __forceinline__ float4 store(float* p, float4 v) {
+    *reinterpret_cast<float4*>(p) = v;
+    return v;
+  }
+};
+template <typename T>
+struct Io16 {
+  __device__ static __forceinline__ float4 load(const T* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const float2 a = F16<T>::unpack(u.x), b = F16<T>::unpack(u.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+  // stores v rounded to T and returns what was stored
+  __device__ static __forceinline__ float4 store(T* p, float4 v) {
+    uint2 u;
+    u.x = F16<T>::pack(v.x, v.y);
+    u.y = F16<T>::pack(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) = u;
+    const float2 a = F16<T>::unpack(u.x), b = F16<T>::unpack(u.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+};
+template <>
+struct Io<__half> : Io16<__half> {};
+template <>
+struct Io<__nv_bfloat16> : Io16<__nv_bfloat16> {};
+
+// One q8_0 code: round(y / d) half away from zero (y * inv within +-127 and finite)
+__device__ __forceinline__ uint32_t q8_code(float y, float inv) {
+  const float r = y * inv, t = truncf(r);
+  const float c = t + (fabsf(r - t) >= 0.5f ? copysignf(1.f, r) : 0.f);
+  return static_cast<uint32_t>(static_cast<int>(c)) & 0xffu;
+}
+
+// One block of 256 threads per row.
+template <typename TX, typename TH, typename TO>
+__global__ void __launch_bounds__(256)
+    add_rmsnorm_kernel(const TX* __restrict__ x, int64_t ldx, const TH* h, TH* h_out, int64_t ldh,
+                       const float* __restrict__ g, TO* __restrict__ out, int64_t ldo,
+                       __half* __restrict__ scales, int rows, int n, float eps) {
+  griddep_wait_and_release();
+  const int64_t row = blockIdx.x;
+  float ss = 0.f;
+  for (int i = threadIdx.x * 4; i < n; i += 1024) {
+    const float4 a = Io<TX>::load(x + row * ldx + i), b = Io<TH>::load(h + row * ldh + i);
+    const float4 v = Io<TH>::store(h_out + row * ldh + i, make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w));
+    ss += v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
+  }
+  __shared__ float red[8];
+  ss = warp_sum(ss);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
+  __syncthreads();
+  float tot = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) tot += red[w];
+  const float sc = rsqrtf(tot / static_cast<float>(n) + eps);
+  for (int i0 = 0; i0 < n; i0 += 1024) {  // (all threads: the 8 of a q8_0 block take part together)
+    const int i = i0 + threadIdx.x * 4;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n) {
+      const float4 v = Io<TH>::load(h_out + row * ldh + i), gg = *reinterpret_cast<const float4*>(g + i);
+      y = make_float4(v.x * sc * gg.x, v.y * sc * gg.y, v.z * sc * gg.z, v.w * sc * gg.w);
+    }
+    if constexpr (sizeof(TO) == 1) {
+      float amax = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
+      // a NaN or infinity makes the sum of 0 * y a NaN
+      float bad = 0.f * y.x + 0.f * y.y + 0.f * y.z + 0.f * y.w;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        bad += __shfl_xor_sync(0xffffffffu, bad, o);
+      }
+      if (i < n) {
+        const bool fine = bad == 0.f;
+        // (a subnormal d is 0 in fp16, whatever the codes; its reciprocal could overflow)
+        const float d = amax / 127.f, inv = fine && d >= 1.1754944e-38f ? 1.f / d : 0.f;
+        uint32_t c = 0;
+        if (fine)
+          c = q8_code(y.x, inv) | q8_code(y.y, inv) << 8 | q8_code(y.z, inv) << 16 | q8_code(y.w, inv) << 24;
+        *reinterpret_cast<uint32_t*>(out + row * ldo + i) = c;
+        if ((threadIdx.x & 7) == 0)
+          scales[static_cast<int64_t>(i >> 5) * rows + row] = __float2half_rn(fine ? d : __int_as_float(0x7fffffff));
+      }
+    } else if (i < n) {
+      Io<TO>::store(out + row * ldo + i, y);
+    }
+  }
+}
+
+struct Args {
+  const void* x;
+  int64_t ldx;
+  const void* h;
+  void* h_out;
+  int64_t ldh;
+  const float* g;
+  void* out;
+  int64_t ldo;
+  void* scales;
+  int rows, n;
+  float eps;
+  cudaStream_t s;
+};
+
+template <typename TX, typename TH, typename TO>
+cudaError_t launch(const Args& a) {
+  return launch_pdl(add_rmsnorm_kernel<TX, TH, TO>, dim3(a.rows), dim3(256), 0, a.s,
+                    static_cast<const TX*>(a.x), a.ldx, static_cast<const TH*>(a.h), static_cast<TH*>(a.h_out), a.ldh,
+                    a.g, static_cast<TO*>(a.out), a.ldo, static_cast<__half*>(a.scales), a.rows, a.n, a.eps);
+}
+template <typename TX, typename TH>
+cudaError_t by_out(const Args& a, int out_dtype) {
+  if (out_dtype == KVA_Q8_0) return launch<TX, TH, int8_t>(a);
+  return out_dtype == KVA_F16 ? launch<TX, TH, __half>(a) : launch<TX, TH, __nv_bfloat16>(a);
+}
+template <typename TX>
+cudaError_t by_h(const Args& a, int h_dtype, int out_dtype) {
+  if (h_dtype == KVA_F32) return by_out<TX, float>(a, out_dtype);
+  return h_dtype == KVA_F16 ? by_out<TX, __half>(a, out_dtype) : by_out<TX, __nv_bfloat16>(a, out_dtype);
+}
+bool is_float_dtype(int t) { return t == KVA_F32 || t == KVA_F16 || t == KVA_BF16; }
+
+}  // namespace
+}  // namespace kva
+
+extern "C" int kva_op_add_rmsnorm(const void* x, int32_t x_dtype, int64_t ldx, const void* h, void* h_out,
+                                  int32_t h_dtype, int64_t ldh, const float* g, void* out, int32_t out_dtype,
+                                  int64_t ldo, void* scales, int32_t rows, int32_t n, float eps, void* stream) {
+  using namespace kva;
+  if (rows < 0 || n <= 0 || !(eps >= 0.f)) return KVA_ERR_INVALID_ARG;
+  if (!is_float_dtype(x_dtype) || !is_float_dtype(h_dtype)) return KVA_ERR_INVALID_ARG;
+  if (out_dtype != KVA_BF16 && out_dtype != KVA_F16 && out_dtype != KVA_Q8_0) return KVA_ERR_INVALID_ARG;
+  if (n > 16 * 1024) return KVA_ERR_UNSUPPORTED;
+  const bool q8 = out_dtype == KVA_Q8_0;
+  if (q8 && n % 32) return KVA_ERR_UNSUPPORTED;
+  if (rows == 0) return KVA_OK;
+  if (!x || !h || !h_out || !g || !out || q8 != (scales != nullptr)) return KVA_ERR_INVALID_ARG;
+  if (ldx < n || ldh < n || ldo < n) return KVA_ERR_INVALID_ARG;
+  if (n % 4 || ldx % 4 || ldh % 4 || ldo % (q8 ? 16 : 4)) return KVA_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(h) | reinterpret_cast<uintptr_t>(h_out) |
+       reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(out)) & 15u)
+    return KVA_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(scales) & 1u) return KVA_ERR_ALIGNMENT;
+  const Args a{x, ldx, h, h_out, ldh, g, out, ldo, scales, rows, n, eps, static_cast<cudaStream_t>(stream)};
+  const cudaError_t r = x_dtype == KVA_F32   ? by_h<float>(a, h_dtype, out_dtype)
+                        : x_dtype == KVA_F16 ? by_h<__half>(a, h_dtype, out_dtype)
+                                             : by_h<__nv_bfloat16>(a, h_dtype, out_dtype);
+  return r == cudaSuccess ? KVA_OK : KVA_ERR_CUDA;
+}

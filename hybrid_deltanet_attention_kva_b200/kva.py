@@ -6,6 +6,7 @@ caller owns them); streams default to torch's current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from typing import Dict, Optional, Sequence
@@ -80,6 +81,19 @@ class KvaLastParams(C.Structure):
     _fields_ = [("attn_n_q", C.c_int32), ("gdn_norm_w", C.c_void_p), ("q_norm_g", C.c_void_p)]
 
 
+class KvaGdnForwardArgs(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("n_seq", C.c_int32), ("T", C.c_int32), ("n_k", C.c_int32),
+                ("n_v", C.c_int32), ("d", C.c_int32), ("q", C.c_void_p), ("k", C.c_void_p),
+                ("v", C.c_void_p), ("q_ld", C.c_int64), ("q_seq", C.c_int64), ("k_ld", C.c_int64),
+                ("k_seq", C.c_int64), ("v_ld", C.c_int64), ("v_seq", C.c_int64), ("gb", C.c_void_p),
+                ("state_in", C.c_void_p), ("state_out", C.c_void_p), ("out", C.c_void_p),
+                ("out_ld", C.c_int64), ("out_seq", C.c_int64), ("lens", C.POINTER(C.c_int32)),
+                ("scale", C.c_float)]
+
+
+GDN_MAX_SEQ = 256
+LOGPROB_MAX_TOP = 32
+
 ST_NAMES = ("rmsnorm", "gemm_trunk", "attention", "gemm_heads", "gdn_prepare", "gdn_tail",
             "gdn_scan", "kv_write", "last_token")
 ST_COUNT = len(ST_NAMES)
@@ -129,6 +143,9 @@ def _load() -> C.CDLL:
                                    I32, I32, P, P]),
         "kva_op_attention": (I32, [I32, P, I64, P, I64, I32, I32, I32, P]),
         "kva_op_gdn_scan": (I32, [P, P, P, P, I32, I32, I32, I32, I32, I32, P]),
+        "kva_op_gdn_forward": (I32, [C.POINTER(KvaGdnForwardArgs), P, P]),
+        "kva_op_add_rmsnorm": (I32, [P, I32, I64, P, P, I32, I64, P, P, I32, I64, P, I32, I32, F32, P]),
+        "kva_op_token_logprobs": (I32, [P, I32, I64, I32, I32, P, P, P, P, I32, P, P, P]),
         "kva_gdn_layer_update_noalloc": (I32, [P, I64, I32, I32, I32, I32, P, P, P, P, P, F32, P]),
         "kva_test_gemm_wait_timeout": (I32, [I32, P, P, P, I32, I32, I32, P, P]),
         "kva_gdn_layer_update_noalloc_status": (I32, [P, C.POINTER(I32)]),
@@ -146,7 +163,7 @@ EXPORTED = ("kva_init", "kva_workspace_bytes", "kva_prefill_ubatch", "kva_update
             "kva_get_device_status", "kva_stats", "kva_heads_fused", "kva_free", "kva_strerror",
             "kva_profile_enable", "kva_profile_read",
             "kva_op_rmsnorm", "kva_op_gemm", "kva_op_gemm_q8_0", "kva_op_gemm_q4_0", "kva_op_attention",
-            "kva_op_gdn_scan",
+            "kva_op_gdn_scan", "kva_op_gdn_forward", "kva_op_add_rmsnorm", "kva_op_token_logprobs",
             "kva_gdn_layer_update_noalloc", "kva_gdn_layer_update_noalloc_status",
             "kva_test_gemm_wait_timeout")
 
@@ -429,6 +446,123 @@ def kva_op_gdn_scan(k: torch.Tensor, v: torch.Tensor, gb: torch.Tensor, state: t
     T = k.shape[-2]
     _check(_lib.kva_op_gdn_scan(_ptr(k), _ptr(v), _ptr(gb), _ptr(state), n_seq, n_layers, T, n_k,
                                 n_v, d, _stream(stream)), "kva_op_gdn_scan")
+
+
+def _one_device(stream, *tensors):
+    """The stream to launch on (given, or the current one of the tensors' device) and a context
+    in which that device is current.  Every tensor must be on that one CUDA device."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and (t.device != dev or not t.is_cuda):
+            raise ValueError("the tensors must be on one CUDA device")
+    here = dev.index == torch.cuda.current_device()
+    s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    return s, contextlib.nullcontext() if here else torch.cuda.device(dev)
+
+
+def _dense(t: Optional[torch.Tensor], shape, dtype, what: str) -> Optional[int]:
+    """Pointer of a contiguous tensor of this shape and dtype (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, shape, what: str):
+    """(pointer, row stride) of a 2-D tensor of this shape whose rows are contiguous."""
+    if tuple(t.shape) != tuple(shape) or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a row-major tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def kva_op_gdn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gb: torch.Tensor,
+                       state_in: torch.Tensor, state_out: torch.Tensor, out: torch.Tensor, *,
+                       lens: Optional[Sequence[int]] = None, scale: float = 1.0,
+                       err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gated delta rule with its readout for every token of n_seq sequences (see
+    include/kva_ops.h).  q, k [n_seq, T, n_k, d] and v, out [n_seq, T, n_v, d] in one 16-bit
+    dtype, each token's heads contiguous (views into a wider row are fine); gb fp32
+    [n_seq, 2, n_v, T] (g, then beta); state_in and state_out fp32 [n_seq, n_v, d, d] (the same
+    tensor: in place); lens: tokens of each sequence (host integers), default all T."""
+    n_seq, T, n_k, d = q.shape
+    n_v = v.shape[2]
+    s, on = _one_device(stream, q, k, v, gb, state_in, state_out, out, err)
+    a = KvaGdnForwardArgs(dtype=_DT[q.dtype], n_seq=n_seq, T=T, n_k=n_k, n_v=n_v, d=d, scale=scale)
+    for name, t, heads in (("q", q, n_k), ("k", k, n_k), ("v", v, n_v), ("out", out, n_v)):
+        if t.dtype != q.dtype or tuple(t.shape) != (n_seq, T, heads, d):
+            raise ValueError(f"{name} must be {q.dtype} {(n_seq, T, heads, d)}, got {t.dtype} {tuple(t.shape)}")
+        st = t.stride()
+        if st[3] != 1 or (heads > 1 and st[2] != d):
+            raise ValueError(f"the heads of a token of {name} must be contiguous")
+        setattr(a, name, t.data_ptr())
+        # a stride over a single token or sequence is never used: one that passes the checks
+        ld = st[1] if T > 1 else heads * d
+        setattr(a, name + "_ld", ld)
+        setattr(a, name + "_seq", st[0] if n_seq > 1 else T * ld)
+    a.gb = _dense(gb, (n_seq, 2, n_v, T), torch.float32, "gb")
+    a.state_in = _dense(state_in, (n_seq, n_v, d, d), torch.float32, "state_in")
+    a.state_out = _dense(state_out, (n_seq, n_v, d, d), torch.float32, "state_out")
+    if lens is not None:
+        if len(lens) != n_seq:
+            raise ValueError(f"lens must hold {n_seq} lengths, got {len(lens)}")
+        if n_seq and not 0 <= min(lens) <= max(lens) <= T:
+            raise ValueError(f"lens must lie in 0..{T}")
+        a.lens = (C.c_int32 * max(1, n_seq))(*lens)
+    with on:
+        _check(_lib.kva_op_gdn_forward(C.byref(a), _dense(err, (1,), torch.int32, "err"), s),
+               "kva_op_gdn_forward")
+
+
+def kva_op_add_rmsnorm(x: torch.Tensor, h: torch.Tensor, g: torch.Tensor, h_out: torch.Tensor,
+                       out: torch.Tensor, *, scales: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                       stream=None) -> None:
+    """h_out = h + x and out = RMSNorm(h_out) * g (see include/kva_ops.h): x, h, h_out, out
+    [rows, n] with contiguous rows, g fp32 [n]; h_out may be h.  out bf16 / fp16, or int8 codes
+    with fp16 scales [n / 32, rows] (q8_0, as kva_op_gemm_q8_0 reads it)."""
+    rows, n = x.shape
+    s, on = _one_device(stream, x, h, g, h_out, out, scales)
+    if h_out.dtype != h.dtype:
+        raise ValueError("h and h_out must have one dtype")
+    px, ldx = _rows(x, (rows, n), "x")
+    ph, ldh = _rows(h, (rows, n), "h")
+    pho, ldho = _rows(h_out, (rows, n), "h_out")
+    po, ldo = _rows(out, (rows, n), "out")
+    if rows > 1 and ldh != ldho:
+        raise ValueError("h and h_out must have one row stride")
+    q8 = out.dtype == torch.int8
+    if q8 != (scales is not None):
+        raise ValueError("scales go with int8 codes, and with nothing else")
+    psc = _dense(scales, (n // 32, rows), torch.float16, "scales")
+    with on:
+        _check(_lib.kva_op_add_rmsnorm(px, _DT[x.dtype], ldx, ph, pho, _DT[h.dtype], ldh,
+                                       _dense(g, (n,), torch.float32, "g"), po,
+                                       KVA_Q8_0 if q8 else _DT[out.dtype], ldo, psc, rows, n, float(eps), s),
+               "kva_op_add_rmsnorm")
+
+
+def kva_op_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None,
+                          logprob: Optional[torch.Tensor] = None, *, lse: Optional[torch.Tensor] = None,
+                          entropy: Optional[torch.Tensor] = None, top_id: Optional[torch.Tensor] = None,
+                          top_logprob: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Log probabilities of given tokens, log-sum-exp, entropy and the most probable tokens of
+    rows of logits (see include/kva_ops.h): logits [rows, n_vocab] with contiguous rows, tokens
+    int32 [rows], logprob / lse / entropy fp32 [rows], top_id int32 and top_logprob fp32
+    [rows, n_top]."""
+    rows, V = logits.shape
+    s, on = _one_device(stream, logits, tokens, logprob, lse, entropy, top_id, top_logprob)
+    px, ld = _rows(logits, (rows, V), "logits")
+    n_top = 0 if top_id is None else top_id.shape[-1]
+    if (top_id is None) != (top_logprob is None) or (tokens is None) != (logprob is None):
+        raise ValueError("top_id goes with top_logprob, tokens with logprob")
+    with on:
+        _check(_lib.kva_op_token_logprobs(
+            px, _DT[logits.dtype], ld, rows, V, _dense(tokens, (rows,), torch.int32, "tokens"),
+            _dense(logprob, (rows,), torch.float32, "logprob"), _dense(lse, (rows,), torch.float32, "lse"),
+            _dense(entropy, (rows,), torch.float32, "entropy"), n_top,
+            _dense(top_id, (rows, n_top), torch.int32, "top_id"),
+            _dense(top_logprob, (rows, n_top), torch.float32, "top_logprob"), s), "kva_op_token_logprobs")
 
 
 def kva_gdn_layer_update_noalloc(mixer_in: torch.Tensor, n_k: int, n_v: int, d: int,

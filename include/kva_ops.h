@@ -106,6 +106,82 @@ int kva_op_gdn_scan(const void* k, const void* v, const float* gb, float* state,
                     int32_t n_layers, int32_t T, int32_t n_k, int32_t n_v, int32_t d,
                     void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Exact layers over several tokens: the three steps that run the late layers of the
+ * hybrid model exactly for every token of a short or long run (drafted tokens that are
+ * checked, a ubatch whose answers are compared with the approximated ones) around the
+ * caller's projections.  They need no handle and no workspace. */
+
+#define KVA_GDN_MAX_SEQ 256  /* sequences per kva_op_gdn_forward call */
+
+/* Gated delta rule with its readout, for n_seq independent sequences of one layer:
+ *   u_t = beta_t (v_t - e^(g_t) S_(t-1) k_t)
+ *   S_t = e^(g_t) S_(t-1) + u_t k_t^T          (= the recurrence of kva_op_gdn_scan)
+ *   o_t = scale * S_t q_t
+ * v head h reads k and q head h / (n_v / n_k).  The state is held in fp32 throughout. */
+typedef struct kva_gdn_forward_args {
+  int32_t dtype;          /* 16-bit format of q, k, v and out: KVA_BF16 or KVA_F16 */
+  int32_t n_seq;          /* sequences, 0..KVA_GDN_MAX_SEQ */
+  int32_t T;              /* tokens per sequence (0: state_out is state_in) */
+  int32_t n_k, n_v, d;    /* q / k heads, v heads (a multiple of n_k), head dim 64 or 128 */
+  const void* q;          /* [n_seq, T, n_k, d]: token stride q_ld, sequence stride q_seq */
+  const void* k;          /* [n_seq, T, n_k, d], keys of norm <= 1 (as the prefill makes them) */
+  const void* v;          /* [n_seq, T, n_v, d] */
+  int64_t q_ld, q_seq;    /* in elements, multiples of 8; the heads of a token are contiguous */
+  int64_t k_ld, k_seq;
+  int64_t v_ld, v_seq;
+  const float* gb;        /* [n_seq, 2, n_v, T]: g (log decay), then beta, per v head */
+  const float* state_in;  /* [n_seq, n_v, d, d] */
+  float* state_out;       /* [n_seq, n_v, d, d]; may be state_in (in place), no other overlap */
+  void* out;              /* [n_seq, T, n_v, d]: token stride out_ld, sequence stride out_seq;
+                             overlaps no input */
+  int64_t out_ld, out_seq;
+  const int32_t* lens;    /* HOST [n_seq] tokens of each sequence (0..T), or NULL: all T.  Tokens
+                             past a sequence's length are neither read nor written. */
+  float scale;            /* factor of the readout */
+} kva_gdn_forward_args;
+int kva_op_gdn_forward(const kva_gdn_forward_args* a, int32_t* err, void* stream);
+
+/* The step between two layers: the residual stream takes a layer's output, and the next
+ * layer's input is its RMSNorm.
+ *   h_out[r] = h[r] + x[r], rounded to h_dtype
+ *   y[r]     = h_out[r] / sqrt(mean(h_out[r]^2) + eps) * g
+ * x [rows, ldx] in x_dtype, h and h_out [rows, ldh] in h_dtype (KVA_BF16, KVA_F16 or
+ * KVA_F32); h_out may be h (in place), no other overlap.  y goes to out [rows, ldo]:
+ *   out_dtype KVA_BF16 / KVA_F16: 16-bit values, scales NULL;
+ *   out_dtype KVA_Q8_0: int8 codes and fp16 scales [n / 32, rows] (one 32-wide block of all
+ *     rows contiguous, the layout kva_op_gemm_q8_0 reads), n a multiple of 32: per block of
+ *     32 values d = max|y| / 127, codes round(y / d) half away from zero, d rounded to
+ *     fp16 for storage; a block that holds a NaN or an infinity gets the scale NaN and
+ *     codes 0.
+ * n, ldx, ldh and ldo multiples of 4 (ldo of 16 bytes for q8_0), n <= 16384; pointers
+ * 16-byte aligned (scales: 2). */
+int kva_op_add_rmsnorm(const void* x, int32_t x_dtype, int64_t ldx, const void* h, void* h_out,
+                       int32_t h_dtype, int64_t ldh, const float* g, void* out, int32_t out_dtype,
+                       int64_t ldo, void* scales, int32_t rows, int32_t n, float eps, void* stream);
+
+#define KVA_LOGPROB_MAX_TOP 32
+
+/* Scores of a row of logits: the log softmax at a given token, its normaliser, the entropy
+ * and the n_top most probable tokens.
+ *   logits      [rows, ld] in dtype (KVA_BF16, KVA_F16 or KVA_F32), n_vocab columns used; any ld
+ *               >= n_vocab, pointer aligned to its element
+ *   tokens      int32 [rows] (device) or NULL.  -1: no token given (logprob 0); any other
+ *               value outside 0..n_vocab-1: logprob NaN
+ *   logprob     fp32 [rows]: x[token] - lse (with tokens; NULL without)
+ *   lse         fp32 [rows] or NULL: log sum_j e^x_j
+ *   entropy     fp32 [rows] or NULL: -sum_j p_j log p_j, with 0 log 0 = 0
+ *   top_id      int32 [rows, n_top], top_logprob fp32 [rows, n_top]: the n_top
+ *               (0..KVA_LOGPROB_MAX_TOP) largest logits in descending order, equal ones in
+ *               ascending token order; a row with fewer tokens above -infinity ends with
+ *               id -1 and -infinity.  NULL when n_top is 0.
+ * A logit of -infinity is a token ruled out.  A row of them only has lse and logprobs
+ * -infinity, entropy 0 and no alternatives.  A row that holds a NaN or +infinity gets NaN
+ * everywhere and ids -1.  Sums and results are fp32. */
+int kva_op_token_logprobs(const void* logits, int32_t dtype, int64_t ld, int32_t rows, int32_t n_vocab,
+                          const int32_t* tokens, float* logprob, float* lse, float* entropy,
+                          int32_t n_top, int32_t* top_id, float* top_logprob, void* stream);
+
 /* Limits of kva_gdn_layer_update_noalloc's fixed scratch (about 6.5 MB per GPU). */
 #define KVA_NOALLOC_MAX_T 256    /* tokens per call */
 #define KVA_NOALLOC_MAX_QK 2048  /* n_k * d */
