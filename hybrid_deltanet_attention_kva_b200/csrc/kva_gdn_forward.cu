@@ -25,6 +25,9 @@ struct GdnFwd {
   int32_t lens[KVA_GDN_MAX_SEQ];
 };
 
+// runs of at most this many tokens go token by token
+constexpr int kStepTokens = 8;
+
 // 4 consecutive 16-bit values as floats
 template <typename T>
 __device__ __forceinline__ void load4(float (&f)[4], const T* p) {
@@ -101,9 +104,401 @@ __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constan
     *reinterpret_cast<float4*>(p.state_out + srow + 32 * i) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
 }
 
+// ============================================================================
+// Runs of 16 tokens on mma.sync.  With gam_t = sum_{s<=t} g_s inside a run and S the state at
+// its start,
+//     L[t,s] = beta_t e^(gam_t-gam_s) k_t.k_s (s < t),     Tm = (I + L)^-1 diag(beta),
+//     U      = (V^T - S K^T diag(e^gam)) Tm^T              (column s: the update u_s),
+//     O      = S Q^T diag(e^gam) + U M^T,                  M[t,s] = e^(gam_t-gam_s) q_t.k_s (s <= t),
+//     S     <- e^gam_last S + U diag(e^(gam_last-gam)) K.
+// Tm, M and the decays take no state: two preparing warps form them ahead of the chain.  A
+// chain warp owns 16 rows of S as fp32 accumulator fragments, which are also (packed) the A
+// operand of the next product, so a run passes through registers alone: no barrier between the
+// chain's warps, and no trip of S through shared or tensor memory.
+// ============================================================================
+constexpr int CH = 16;          // tokens a run
+constexpr int ROWS = 64;        // state rows a block
+constexpr int CHAIN = ROWS / 16;  // chain warps
+constexpr int PREP = 2;         // preparing warps: runs of their own parity
+constexpr int AHEAD = 2;        // a preparing warp's runs in flight behind the one it works on
+constexpr int NST = 6;          // stages
+constexpr int kChunkThreads = 32 * (CHAIN + PREP);
+
+template <int D>
+struct Stage {
+  static constexpr int K = 0;                      // [16][D], 16-byte pieces xor-swizzled by row
+  static constexpr int Q = K + CH * D * 2;
+  static constexpr int V = Q + CH * D * 2;         // [16][64], this block's columns
+  static constexpr int TH = V + CH * ROWS * 2;     // Tm as two 16-bit terms, [s][t]
+  static constexpr int TL = TH + CH * CH * 2;
+  static constexpr int M = TL + CH * CH * 2;       // [t][s]
+  static constexpr int EG = M + CH * CH * 2;       // e^gam[16]
+  static constexpr int DEC = EG + CH * 4;          // e^(gam_last - gam)[16]
+  static constexpr int GL = DEC + CH * 4;          // e^gam_last
+  static constexpr int BYTES = GL + 128;
+};
+struct Prep {                                      // per preparing warp: L in fp32, row stride 20
+  static constexpr int LDL = 20;
+  static constexpr int BYTES = CH * LDL * 4;
+};
+template <int D>
+struct Chunk {
+  static constexpr int L = NST * Stage<D>::BYTES;
+  static constexpr int BAR = L + PREP * Prep::BYTES;  // full[NST], empty[NST]
+  static constexpr int MISC = BAR + 2 * NST * 8;      // abort flag
+  static constexpr int BYTES = MISC + 16;
+};
+
+// 16-byte piece c of row r in a tile of W-byte rows (W = 128 or 256): eight rows of one piece
+// index fall on different banks
+template <int W>
+__device__ __forceinline__ uint32_t piece(int r, int c) {
+  return static_cast<uint32_t>(r * W + ((c ^ (r & 7)) << 4));
+}
+// the same in a [16][16] 16-bit tile (32-byte rows)
+__device__ __forceinline__ uint32_t piece16(int r, int c) {
+  return static_cast<uint32_t>(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
+}
+
+// x as two 16-bit terms: hi + lo holds x to the square of the type's half step
+template <typename T>
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = F16<T>::pack(x, y);
+  const float2 h = F16<T>::unpack(hi);
+  lo = F16<T>::pack(x - h.x, y - h.y);
+}
+// accumulator fragments of two neighbouring 8-column tiles as an A operand (16 x 16)
+template <typename T>
+__device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], uint32_t (&hi)[4],
+                                        uint32_t (&lo)[4]) {
+  split2<T>(c0[0], c0[1], hi[0], lo[0]);
+  split2<T>(c0[2], c0[3], hi[1], lo[1]);
+  split2<T>(c1[0], c1[1], hi[2], lo[2]);
+  split2<T>(c1[2], c1[3], hi[3], lo[3]);
+}
+template <typename T>
+__device__ __forceinline__ void mma2(float (&d0)[4], float (&d1)[4], const uint32_t (&a)[4], const uint32_t (&b)[4],
+                                     int i0, int i1, int i2, int i3) {
+  const uint32_t b0[2] = {b[i0], b[i1]}, b1[2] = {b[i2], b[i3]};
+  F16<T>::mma(d0, a, b0);
+  F16<T>::mma(d1, a, b1);
+}
+
 template <typename T, int D>
-cudaError_t launch(const GdnFwd& p, int n_seq, cudaStream_t s) {
-  return launch_pdl(gdn_recurrent_kernel<T, D>, dim3(p.n_v * (D / 32), n_seq), dim3(256), 0, s, p);
+__device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int seq, int len, int pw, int lane,
+                             volatile int* abort_flag) {
+  using St = Stage<D>;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Chunk<D>::BAR);
+  uint64_t* empty = full + NST;
+  const int kh = h / (p.n_v / p.n_k), n_runs = (len + CH - 1) / CH;
+  const T* q = static_cast<const T*>(p.q) + seq * p.q_seq + kh * D;
+  const T* k = static_cast<const T*>(p.k) + seq * p.k_seq + kh * D;
+  const T* v = static_cast<const T*>(p.v) + seq * p.v_seq + h * D + half * ROWS;
+  const float* g = p.gb + (static_cast<int64_t>(seq) * 2 * p.n_v + h) * p.T;
+  const float* b = g + static_cast<int64_t>(p.n_v) * p.T;
+  float* Ls = reinterpret_cast<float*>(sm + Chunk<D>::L + pw * Prep::BYTES);
+  const uint32_t base = smem_u32(sm);
+
+  auto load = [&](int c) {  // rows past the sequence's end are zero, never read
+    const uint32_t st = base + (c % NST) * St::BYTES;
+    constexpr int PK = D / 8, PV = ROWS / 8;
+#pragma unroll
+    for (int i = 0; i < CH * PK / 32; ++i) {
+      const int r = (i * 32 + lane) / PK, x = (i * 32 + lane) % PK;
+      const int64_t t = c * CH + r;
+      const uint32_t n = t < len ? 16u : 0u;
+      cp_async16(st + St::K + piece<2 * D>(r, x), n ? k + t * p.k_ld + 8 * x : k, n);
+      cp_async16(st + St::Q + piece<2 * D>(r, x), n ? q + t * p.q_ld + 8 * x : q, n);
+    }
+#pragma unroll
+    for (int i = 0; i < CH * PV / 32; ++i) {
+      const int r = (i * 32 + lane) / PV, x = (i * 32 + lane) % PV;
+      const int64_t t = c * CH + r;
+      const uint32_t n = t < len ? 16u : 0u;
+      cp_async16(st + St::V + piece<2 * ROWS>(r, x), n ? v + t * p.v_ld + 8 * x : v, n);
+    }
+  };
+  float g_next = 0.f, b_next = 0.f;
+  auto load_gates = [&](int c) {
+    const int t = c * CH + lane;
+    const bool on = lane < CH && t < len;
+    g_next = on ? g[t] : 0.f;
+    b_next = on ? b[t] : 0.f;
+  };
+  for (int j = 0; j < AHEAD; ++j) {
+    if (pw + PREP * j < n_runs) load(pw + PREP * j);
+    cp_async_commit();
+  }
+  load_gates(pw);
+  const int mi = lane >> 3, lr = lane & 7, gr = lane >> 2, cq = lane & 3;
+
+  for (int c = pw; c < n_runs; c += PREP) {
+    const int cn = c + PREP * AHEAD;
+    if (cn < n_runs) {
+      if (cn >= NST && !mbar_wait(&empty[cn % NST], (cn / NST - 1) & 1, abort_flag)) {
+        *abort_flag = 1;
+        set_device_error(p.err, KVA_DEV_WAIT_TIMEOUT);
+        break;
+      }
+      load(cn);
+    }
+    cp_async_commit();
+    float gt = g_next;
+    const float bt = b_next;
+    load_gates(c + PREP);  // (past the last run: zeros)
+    // e^g is 0 in fp32 from -104 on; the clamp keeps -infinity out of the differences
+    gt = gt < -1000.f ? -1000.f : gt;
+    // cumulative decays in 64 bits: differences of neighbours keep fp32's precision however far
+    // the sum has run
+    double gam = gt;
+#pragma unroll
+    for (int o = 1; o < CH; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, gam, o);
+      if (lane >= o) gam += y;
+    }
+    const double last = __shfl_sync(0xffffffffu, gam, CH - 1);
+    uint8_t* st = sm + (c % NST) * St::BYTES;
+    const uint32_t sst = base + (c % NST) * St::BYTES;
+    if (lane < CH) {
+      reinterpret_cast<float*>(st + St::EG)[lane] = expf(static_cast<float>(gam));
+      reinterpret_cast<float*>(st + St::DEC)[lane] = expf(static_cast<float>(last - gam));
+      if (lane == 0) *reinterpret_cast<float*>(st + St::GL) = expf(static_cast<float>(last));
+    }
+    // pair decays of this thread's fragment elements (t = gr + 8 a, s = 8 i + 2 cq + e)
+    float pd[2][4];
+    {
+      const double t0 = __shfl_sync(0xffffffffu, gam, gr), t1 = __shfl_sync(0xffffffffu, gam, gr + 8);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int s = 8 * i + 2 * cq + e;
+          const double gs = __shfl_sync(0xffffffffu, gam, s);
+          pd[i][e] = s <= gr ? expf(static_cast<float>(t0 - gs)) : 0.f;
+          pd[i][2 + e] = s <= gr + 8 ? expf(static_cast<float>(t1 - gs)) : 0.f;
+        }
+    }
+    cp_async_wait<AHEAD>();
+    __syncwarp();
+    // K K^T and Q K^T: the K fragments serve as A and as B
+    float kk[2][4] = {}, qk[2][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t a[4], x[4];
+      ldmatrix_x4(a, sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
+      ldmatrix_x4(x, sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
+      mma2<T>(kk[0], kk[1], a, a, 0, 2, 1, 3);
+      mma2<T>(qk[0], qk[1], x, a, 0, 2, 1, 3);
+    }
+    const float bt0 = __shfl_sync(0xffffffffu, bt, gr), bt1 = __shfl_sync(0xffffffffu, bt, gr + 8);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int s = 8 * i + 2 * cq;
+      *reinterpret_cast<float2*>(Ls + gr * Prep::LDL + s) =
+          make_float2(s < gr ? bt0 * pd[i][0] * kk[i][0] : 0.f, s + 1 < gr ? bt0 * pd[i][1] * kk[i][1] : 0.f);
+      *reinterpret_cast<float2*>(Ls + (gr + 8) * Prep::LDL + s) =
+          make_float2(s < gr + 8 ? bt1 * pd[i][2] * kk[i][2] : 0.f, s + 1 < gr + 8 ? bt1 * pd[i][3] * kk[i][3] : 0.f);
+      // (pd is 0 above the diagonal, but 0 times an infinite product would not be)
+      *reinterpret_cast<uint32_t*>(st + St::M + piece16(gr, i) + 4 * cq) =
+          F16<T>::pack(s <= gr ? pd[i][0] * qk[i][0] : 0.f, s + 1 <= gr ? pd[i][1] * qk[i][1] : 0.f);
+      *reinterpret_cast<uint32_t*>(st + St::M + piece16(gr + 8, i) + 4 * cq) =
+          F16<T>::pack(s <= gr + 8 ? pd[i][2] * qk[i][2] : 0.f, s + 1 <= gr + 8 ? pd[i][3] * qk[i][3] : 0.f);
+    }
+    __syncwarp();
+    // (I + L)^-1 by forward substitution in fp32, one column a lane; times beta of the column
+    if (lane < CH) {
+      float x[CH];
+#pragma unroll
+      for (int t = 0; t < CH; ++t) x[t] = t == lane ? 1.f : 0.f;
+#pragma unroll
+      for (int t = 1; t < CH; ++t) {
+        float l[CH];
+#pragma unroll
+        for (int s = 0; s < t; s += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(Ls + t * Prep::LDL + s);
+          l[s] = f.x;
+          l[s + 1] = f.y;
+          l[s + 2] = f.z;
+          l[s + 3] = f.w;
+        }
+#pragma unroll
+        for (int s = 0; s < t; ++s) x[t] = fmaf(-l[s], x[s], x[t]);
+      }
+#pragma unroll
+      for (int t = 0; t < CH; ++t) {
+        uint32_t hi, lo;
+        split2<T>(x[t] * bt, 0.f, hi, lo);
+        const uint32_t o = piece16(t, lane >> 3) + (lane & 7) * 2;
+        *reinterpret_cast<uint16_t*>(st + St::TH + o) = static_cast<uint16_t>(hi);
+        *reinterpret_cast<uint16_t*>(st + St::TL + o) = static_cast<uint16_t>(lo);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[c % NST]);
+  }
+  cp_async_wait<0>();
+}
+
+template <typename T, int D>
+__device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int seq, int len, int warp, int lane,
+                           volatile int* abort_flag) {
+  using St = Stage<D>;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Chunk<D>::BAR);
+  uint64_t* empty = full + NST;
+  const int n_runs = (len + CH - 1) / CH;
+  const int mi = lane >> 3, lr = lane & 7, gr = lane >> 2, cq = lane & 3;
+  const uint32_t base = smem_u32(sm);
+  const int64_t srow = ((static_cast<int64_t>(seq) * p.n_v + h) * D + half * ROWS + warp * 16 + gr) * D + 2 * cq;
+  float S[D / 8][4];
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j) {
+    const float2 a = *reinterpret_cast<const float2*>(p.state_in + srow + 8 * j);
+    const float2 c = *reinterpret_cast<const float2*>(p.state_in + srow + 8 * D + 8 * j);
+    S[j][0] = a.x;
+    S[j][1] = a.y;
+    S[j][2] = c.x;
+    S[j][3] = c.y;
+  }
+  T* out = static_cast<T*>(p.out) + seq * p.out_seq + h * D + half * ROWS + warp * 16 + 2 * cq;
+
+  for (int c = 0; c < n_runs; ++c) {
+    if (!mbar_wait(&full[c % NST], (c / NST) & 1, abort_flag)) {
+      *abort_flag = 1;
+      set_device_error(p.err, KVA_DEV_WAIT_TIMEOUT);
+      break;
+    }
+    const uint8_t* st = sm + (c % NST) * St::BYTES;
+    const uint32_t sst = base + (c % NST) * St::BYTES;
+    // Y = S K^T (both terms of S), Z = S Q^T (the first term)
+    float y[2][4] = {}, yl[2][4] = {}, z[2][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t ah[4], al[4], kf[4], qf[4];
+      split_a<T>(S[2 * ks], S[2 * ks + 1], ah, al);
+      ldmatrix_x4(kf, sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
+      ldmatrix_x4(qf, sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
+      mma2<T>(y[0], y[1], ah, kf, 0, 2, 1, 3);
+      mma2<T>(yl[0], yl[1], al, kf, 0, 2, 1, 3);
+      mma2<T>(z[0], z[1], ah, qf, 0, 2, 1, 3);
+    }
+    // W = V^T - Y diag(e^gam)
+    uint32_t vf[4], wh[4], wl[4];
+    ldmatrix_x4_trans(vf, sst + St::V + piece<2 * ROWS>((mi >> 1) * 8 + lr, 2 * warp + (mi & 1)));
+    {
+      float w[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 e = *reinterpret_cast<const float2*>(st + St::EG + (8 * i + 2 * cq) * 4);
+        const float2 v0 = F16<T>::unpack(vf[2 * i]), v1 = F16<T>::unpack(vf[2 * i + 1]);
+        w[i][0] = v0.x - e.x * (y[i][0] + yl[i][0]);
+        w[i][1] = v0.y - e.y * (y[i][1] + yl[i][1]);
+        w[i][2] = v1.x - e.x * (y[i][2] + yl[i][2]);
+        w[i][3] = v1.y - e.y * (y[i][3] + yl[i][3]);
+        z[i][0] *= e.x;
+        z[i][1] *= e.y;
+        z[i][2] *= e.x;
+        z[i][3] *= e.y;
+      }
+      split_a<T>(w[0], w[1], wh, wl);
+    }
+    // U = W Tm^T
+    float u[2][4] = {}, ul[2][4] = {};
+    {
+      uint32_t th[4], tl[4];
+      ldmatrix_x4(th, sst + St::TH + piece16((mi & 1) * 8 + lr, mi >> 1));
+      ldmatrix_x4(tl, sst + St::TL + piece16((mi & 1) * 8 + lr, mi >> 1));
+      mma2<T>(u[0], u[1], wh, th, 0, 2, 1, 3);
+      mma2<T>(ul[0], ul[1], wl, th, 0, 2, 1, 3);
+      mma2<T>(ul[0], ul[1], wh, tl, 0, 2, 1, 3);
+    }
+    uint32_t uh[4], dh[4], dl[4];
+    {
+      float dd[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 e = *reinterpret_cast<const float2*>(st + St::DEC + (8 * i + 2 * cq) * 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[i][j] += ul[i][j];
+        uh[2 * i] = F16<T>::pack(u[i][0], u[i][1]);
+        uh[2 * i + 1] = F16<T>::pack(u[i][2], u[i][3]);
+        dd[i][0] = u[i][0] * e.x;
+        dd[i][1] = u[i][1] * e.y;
+        dd[i][2] = u[i][2] * e.x;
+        dd[i][3] = u[i][3] * e.y;
+      }
+      split_a<T>(dd[0], dd[1], dh, dl);
+    }
+    // S <- e^gam_last S + U diag(dec) K
+    const float gl = *reinterpret_cast<const float*>(st + St::GL);
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[j][e] *= gl;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t kf[4];
+      ldmatrix_x4_trans(kf, sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
+      mma2<T>(S[2 * ks], S[2 * ks + 1], dh, kf, 0, 1, 2, 3);
+      mma2<T>(S[2 * ks], S[2 * ks + 1], dl, kf, 0, 1, 2, 3);
+    }
+    // O = Z diag(e^gam) + U M^T, written token-major
+    {
+      uint32_t mf[4];
+      ldmatrix_x4(mf, sst + St::M + piece16((mi & 1) * 8 + lr, mi >> 1));
+      mma2<T>(z[0], z[1], uh, mf, 0, 2, 1, 3);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[c % NST]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t o0 = movmatrix_trans(F16<T>::pack(p.scale * z[i][0], p.scale * z[i][1]));
+      const uint32_t o1 = movmatrix_trans(F16<T>::pack(p.scale * z[i][2], p.scale * z[i][3]));
+      const int64_t t = c * CH + 8 * i + gr;
+      if (t < len) {
+        *reinterpret_cast<uint32_t*>(out + t * p.out_ld) = o0;
+        *reinterpret_cast<uint32_t*>(out + t * p.out_ld + 8) = o1;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j) {
+    *reinterpret_cast<float2*>(p.state_out + srow + 8 * j) = make_float2(S[j][0], S[j][1]);
+    *reinterpret_cast<float2*>(p.state_out + srow + 8 * D + 8 * j) = make_float2(S[j][2], S[j][3]);
+  }
+}
+
+// grid (n_v * D / 64, n_seq): 64 state rows of one head, four chain warps and two preparing ones
+template <typename T, int D>
+__global__ void __launch_bounds__(kChunkThreads, 2) gdn_chunk_kernel(const __grid_constant__ GdnFwd p) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Chunk<D>::BAR);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Chunk<D>::MISC);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int HALVES = D / ROWS;
+  const int h = blockIdx.x / HALVES, half = blockIdx.x % HALVES, seq = blockIdx.y;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&bars[i], 1);
+      mbar_init(&bars[NST + i], CHAIN);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  griddep_wait_and_release();
+  const int len = p.has_lens ? p.lens[seq] : p.T;
+  if (warp < CHAIN) chain_runs<T, D>(p, sm, h, half, seq, len, warp, lane, abort_flag);
+  else prepare_runs<T, D>(p, sm, h, half, seq, len, warp - CHAIN, lane, abort_flag);
+}
+
+template <typename T, int D>
+cudaError_t launch(const GdnFwd& p, int n_seq, int longest, cudaStream_t s) {
+  if (longest <= kStepTokens)
+    return launch_pdl(gdn_recurrent_kernel<T, D>, dim3(p.n_v * (D / 32), n_seq), dim3(256), 0, s, p);
+  const cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Chunk<D>::BYTES);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(gdn_chunk_kernel<T, D>, dim3(p.n_v * (D / ROWS), n_seq), dim3(kChunkThreads), Chunk<D>::BYTES, s, p);
 }
 
 bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -137,11 +532,15 @@ extern "C" int kva_op_gdn_forward(const kva_gdn_forward_args* a, int32_t* err, v
   if (!a16(a->state_in) || !a16(a->state_out)) return KVA_ERR_ALIGNMENT;
   GdnFwd p;
   p.has_lens = a->lens != nullptr;
-  if (a->lens)
+  int longest = a->T;
+  if (a->lens) {
+    longest = 0;
     for (int i = 0; i < a->n_seq; ++i) {
       if (a->lens[i] < 0 || a->lens[i] > a->T) return KVA_ERR_INVALID_ARG;
       p.lens[i] = a->lens[i];
+      if (a->lens[i] > longest) longest = a->lens[i];
     }
+  }
   p.q = a->q;
   p.k = a->k;
   p.v = a->v;
@@ -165,7 +564,7 @@ extern "C" int kva_op_gdn_forward(const kva_gdn_forward_args* a, int32_t* err, v
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f16 = a->dtype == KVA_F16;
   const cudaError_t r = a->d == 128
-                            ? (f16 ? launch<__half, 128>(p, a->n_seq, s) : launch<__nv_bfloat16, 128>(p, a->n_seq, s))
-                            : (f16 ? launch<__half, 64>(p, a->n_seq, s) : launch<__nv_bfloat16, 64>(p, a->n_seq, s));
+                            ? (f16 ? launch<__half, 128>(p, a->n_seq, longest, s) : launch<__nv_bfloat16, 128>(p, a->n_seq, longest, s))
+                            : (f16 ? launch<__half, 64>(p, a->n_seq, longest, s) : launch<__nv_bfloat16, 64>(p, a->n_seq, longest, s));
   return r == cudaSuccess ? KVA_OK : KVA_ERR_CUDA;
 }
