@@ -121,7 +121,7 @@ constexpr int ROWS = 64;        // state rows a block
 constexpr int CHAIN = ROWS / 16;  // chain warps
 constexpr int PREP = 2;         // preparing warps: runs of their own parity
 constexpr int AHEAD = 2;        // a preparing warp's runs in flight behind the one it works on
-constexpr int NST = 6;          // stages
+constexpr int NST = 8;          // stages: the run of AHEAD + 1 own steps back is consumed when its place is needed
 constexpr int kChunkThreads = 32 * (CHAIN + PREP);
 
 template <int D>
@@ -131,15 +131,16 @@ struct Stage {
   static constexpr int V = Q + CH * D * 2;         // [16][64], this block's columns
   static constexpr int TH = V + CH * ROWS * 2;     // Tm as two 16-bit terms, [s][t]
   static constexpr int TL = TH + CH * CH * 2;
-  static constexpr int M = TL + CH * CH * 2;       // [t][s]
-  static constexpr int EG = M + CH * CH * 2;       // e^gam[16]
+  static constexpr int MH = TL + CH * CH * 2;      // M as two 16-bit terms, [t][s]
+  static constexpr int ML = MH + CH * CH * 2;
+  static constexpr int EG = ML + CH * CH * 2;      // e^gam[16]
   static constexpr int DEC = EG + CH * 4;          // e^(gam_last - gam)[16]
   static constexpr int GL = DEC + CH * 4;          // e^gam_last
   static constexpr int BYTES = GL + 128;
 };
-struct Prep {                                      // per preparing warp: L in fp32, row stride 20
+struct Prep {                                      // per preparing warp: L in fp32 (row stride 20), beta
   static constexpr int LDL = 20;
-  static constexpr int BYTES = CH * LDL * 4;
+  static constexpr int BYTES = (CH * LDL + CH) * 4;
 };
 template <int D>
 struct Chunk {
@@ -176,12 +177,22 @@ __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[
   split2<T>(c1[0], c1[1], hi[2], lo[2]);
   split2<T>(c1[2], c1[3], hi[3], lo[3]);
 }
+// D += A B on 16 x 8 x 16 tiles: registers to registers, free to be scheduled
+__device__ __forceinline__ void mma_tile(__half, float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tile(__nv_bfloat16, float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 template <typename T>
 __device__ __forceinline__ void mma2(float (&d0)[4], float (&d1)[4], const uint32_t (&a)[4], const uint32_t (&b)[4],
                                      int i0, int i1, int i2, int i3) {
-  const uint32_t b0[2] = {b[i0], b[i1]}, b1[2] = {b[i2], b[i3]};
-  F16<T>::mma(d0, a, b0);
-  F16<T>::mma(d1, a, b1);
+  mma_tile(T(), d0, a, b[i0], b[i1]);
+  mma_tile(T(), d1, a, b[i2], b[i3]);
 }
 
 template <typename T, int D>
@@ -199,23 +210,38 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
   float* Ls = reinterpret_cast<float*>(sm + Chunk<D>::L + pw * Prep::BYTES);
   const uint32_t base = smem_u32(sm);
 
+  // a lane copies one 16-byte column of every RK-th (V: RV-th) row of a run
+  constexpr int PK = D / 8, PV = ROWS / 8, RK = 32 / PK, RV = 32 / PV;
+  const int xk = lane % PK, rk = lane / PK, xv = lane % PV, rv = lane / PV;
   auto load = [&](int c) {  // rows past the sequence's end are zero, never read
     const uint32_t st = base + (c % NST) * St::BYTES;
-    constexpr int PK = D / 8, PV = ROWS / 8;
+    const int64_t t0 = static_cast<int64_t>(c) * CH;
+    const T* kp = k + (t0 + rk) * p.k_ld + 8 * xk;
+    const T* qp = q + (t0 + rk) * p.q_ld + 8 * xk;
+    const T* vp = v + (t0 + rv) * p.v_ld + 8 * xv;
+    if (t0 + CH <= len) {
 #pragma unroll
-    for (int i = 0; i < CH * PK / 32; ++i) {
-      const int r = (i * 32 + lane) / PK, x = (i * 32 + lane) % PK;
-      const int64_t t = c * CH + r;
-      const uint32_t n = t < len ? 16u : 0u;
-      cp_async16(st + St::K + piece<2 * D>(r, x), n ? k + t * p.k_ld + 8 * x : k, n);
-      cp_async16(st + St::Q + piece<2 * D>(r, x), n ? q + t * p.q_ld + 8 * x : q, n);
-    }
+      for (int i = 0; i < CH / RK; ++i) {
+        cp_async16(st + St::K + piece<2 * D>(i * RK + rk, xk), kp, 16);
+        cp_async16(st + St::Q + piece<2 * D>(i * RK + rk, xk), qp, 16);
+        kp += RK * p.k_ld;
+        qp += RK * p.q_ld;
+      }
 #pragma unroll
-    for (int i = 0; i < CH * PV / 32; ++i) {
-      const int r = (i * 32 + lane) / PV, x = (i * 32 + lane) % PV;
-      const int64_t t = c * CH + r;
-      const uint32_t n = t < len ? 16u : 0u;
-      cp_async16(st + St::V + piece<2 * ROWS>(r, x), n ? v + t * p.v_ld + 8 * x : v, n);
+      for (int i = 0; i < CH / RV; ++i) {
+        cp_async16(st + St::V + piece<2 * ROWS>(i * RV + rv, xv), vp, 16);
+        vp += RV * p.v_ld;
+      }
+    } else {
+      for (int i = 0; i < CH / RK; ++i) {
+        const bool on = t0 + i * RK + rk < len;
+        cp_async16(st + St::K + piece<2 * D>(i * RK + rk, xk), on ? kp + i * RK * p.k_ld : k, on ? 16 : 0);
+        cp_async16(st + St::Q + piece<2 * D>(i * RK + rk, xk), on ? qp + i * RK * p.q_ld : q, on ? 16 : 0);
+      }
+      for (int i = 0; i < CH / RV; ++i) {
+        const bool on = t0 + i * RV + rv < len;
+        cp_async16(st + St::V + piece<2 * ROWS>(i * RV + rv, xv), on ? vp + i * RV * p.v_ld : v, on ? 16 : 0);
+      }
     }
   };
   float g_next = 0.f, b_next = 0.f;
@@ -248,34 +274,41 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
     load_gates(c + PREP);  // (past the last run: zeros)
     // e^g is 0 in fp32 from -104 on; the clamp keeps -infinity out of the differences
     gt = gt < -1000.f ? -1000.f : gt;
-    // cumulative decays in 64 bits: differences of neighbours keep fp32's precision however far
-    // the sum has run
-    double gam = gt;
+    // cumulative decays as unevaluated sums of two floats: differences of neighbours keep fp32's
+    // precision however far the sum has run (fp64 costs 3x the time here)
+    float gam = gt, gaml = 0.f;
 #pragma unroll
     for (int o = 1; o < CH; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, gam, o);
-      if (lane >= o) gam += y;
+      const float y = __shfl_up_sync(0xffffffffu, gam, o), yl = __shfl_up_sync(0xffffffffu, gaml, o);
+      if (lane >= o) {
+        const float s = gam + y, r = s - gam;
+        gaml += yl + ((gam - (s - r)) + (y - r));  // the sum's rounding, exactly (Knuth's two-sum)
+        gam = s;
+      }
     }
-    const double last = __shfl_sync(0xffffffffu, gam, CH - 1);
+    const float last = __shfl_sync(0xffffffffu, gam, CH - 1), lastl = __shfl_sync(0xffffffffu, gaml, CH - 1);
     uint8_t* st = sm + (c % NST) * St::BYTES;
     const uint32_t sst = base + (c % NST) * St::BYTES;
     if (lane < CH) {
-      reinterpret_cast<float*>(st + St::EG)[lane] = expf(static_cast<float>(gam));
-      reinterpret_cast<float*>(st + St::DEC)[lane] = expf(static_cast<float>(last - gam));
-      if (lane == 0) *reinterpret_cast<float*>(st + St::GL) = expf(static_cast<float>(last));
+      reinterpret_cast<float*>(st + St::EG)[lane] = expf(gam + gaml);
+      reinterpret_cast<float*>(st + St::DEC)[lane] = expf((last - gam) + (lastl - gaml));
+      Ls[CH * Prep::LDL + lane] = bt;
+      if (lane == 0) *reinterpret_cast<float*>(st + St::GL) = expf(last + lastl);
     }
-    // pair decays of this thread's fragment elements (t = gr + 8 a, s = 8 i + 2 cq + e)
+    // pair decays of this thread's fragment elements (t = gr + 8 a, s = 8 i + 2 cq + e); the fast
+    // exponential is off by 2^-22 + |x| 2^-24, and what is far has no weight
     float pd[2][4];
     {
-      const double t0 = __shfl_sync(0xffffffffu, gam, gr), t1 = __shfl_sync(0xffffffffu, gam, gr + 8);
+      const float t0 = __shfl_sync(0xffffffffu, gam, gr), t0l = __shfl_sync(0xffffffffu, gaml, gr);
+      const float t1 = __shfl_sync(0xffffffffu, gam, gr + 8), t1l = __shfl_sync(0xffffffffu, gaml, gr + 8);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int s = 8 * i + 2 * cq + e;
-          const double gs = __shfl_sync(0xffffffffu, gam, s);
-          pd[i][e] = s <= gr ? expf(static_cast<float>(t0 - gs)) : 0.f;
-          pd[i][2 + e] = s <= gr + 8 ? expf(static_cast<float>(t1 - gs)) : 0.f;
+          const float gs = __shfl_sync(0xffffffffu, gam, s), gsl = __shfl_sync(0xffffffffu, gaml, s);
+          pd[i][e] = s <= gr ? __expf((t0 - gs) + (t0l - gsl)) : 0.f;
+          pd[i][2 + e] = s <= gr + 8 ? __expf((t1 - gs) + (t1l - gsl)) : 0.f;
         }
     }
     cp_async_wait<AHEAD>();
@@ -299,38 +332,51 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
       *reinterpret_cast<float2*>(Ls + (gr + 8) * Prep::LDL + s) =
           make_float2(s < gr + 8 ? bt1 * pd[i][2] * kk[i][2] : 0.f, s + 1 < gr + 8 ? bt1 * pd[i][3] * kk[i][3] : 0.f);
       // (pd is 0 above the diagonal, but 0 times an infinite product would not be)
-      *reinterpret_cast<uint32_t*>(st + St::M + piece16(gr, i) + 4 * cq) =
-          F16<T>::pack(s <= gr ? pd[i][0] * qk[i][0] : 0.f, s + 1 <= gr ? pd[i][1] * qk[i][1] : 0.f);
-      *reinterpret_cast<uint32_t*>(st + St::M + piece16(gr + 8, i) + 4 * cq) =
-          F16<T>::pack(s <= gr + 8 ? pd[i][2] * qk[i][2] : 0.f, s + 1 <= gr + 8 ? pd[i][3] * qk[i][3] : 0.f);
+      uint32_t hi, lo;
+      split2<T>(s <= gr ? pd[i][0] * qk[i][0] : 0.f, s + 1 <= gr ? pd[i][1] * qk[i][1] : 0.f, hi, lo);
+      *reinterpret_cast<uint32_t*>(st + St::MH + piece16(gr, i) + 4 * cq) = hi;
+      *reinterpret_cast<uint32_t*>(st + St::ML + piece16(gr, i) + 4 * cq) = lo;
+      split2<T>(s <= gr + 8 ? pd[i][2] * qk[i][2] : 0.f, s + 1 <= gr + 8 ? pd[i][3] * qk[i][3] : 0.f, hi, lo);
+      *reinterpret_cast<uint32_t*>(st + St::MH + piece16(gr + 8, i) + 4 * cq) = hi;
+      *reinterpret_cast<uint32_t*>(st + St::ML + piece16(gr + 8, i) + 4 * cq) = lo;
     }
     __syncwarp();
-    // (I + L)^-1 by forward substitution in fp32, one column a lane; times beta of the column
+    // (I + L)^-1 in fp32, row r = lane: x (I + L) = e_r from the last column down (x_s is final
+    // when reached and leaves every earlier column); times beta of the column
     if (lane < CH) {
-      float x[CH];
+      float x[CH], bb[CH];
 #pragma unroll
-      for (int t = 0; t < CH; ++t) x[t] = t == lane ? 1.f : 0.f;
+      for (int s = 0; s < CH; ++s) x[s] = s == lane ? 1.f : 0.f;
 #pragma unroll
-      for (int t = 1; t < CH; ++t) {
+      for (int s = CH - 1; s >= 1; --s) {
         float l[CH];
 #pragma unroll
-        for (int s = 0; s < t; s += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(Ls + t * Prep::LDL + s);
-          l[s] = f.x;
-          l[s + 1] = f.y;
-          l[s + 2] = f.z;
-          l[s + 3] = f.w;
+        for (int i = 0; i < s; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(Ls + s * Prep::LDL + i);
+          l[i] = f.x;
+          l[i + 1] = f.y;
+          l[i + 2] = f.z;
+          l[i + 3] = f.w;
         }
 #pragma unroll
-        for (int s = 0; s < t; ++s) x[t] = fmaf(-l[s], x[s], x[t]);
+        for (int i = 0; i < s; ++i) x[i] = fmaf(-x[s], l[i], x[i]);
       }
 #pragma unroll
-      for (int t = 0; t < CH; ++t) {
-        uint32_t hi, lo;
-        split2<T>(x[t] * bt, 0.f, hi, lo);
-        const uint32_t o = piece16(t, lane >> 3) + (lane & 7) * 2;
-        *reinterpret_cast<uint16_t*>(st + St::TH + o) = static_cast<uint16_t>(hi);
-        *reinterpret_cast<uint16_t*>(st + St::TL + o) = static_cast<uint16_t>(lo);
+      for (int s = 0; s < CH; s += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(Ls + CH * Prep::LDL + s);
+        bb[s] = f.x;
+        bb[s + 1] = f.y;
+        bb[s + 2] = f.z;
+        bb[s + 3] = f.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          split2<T>(x[8 * i + 2 * j] * bb[8 * i + 2 * j], x[8 * i + 2 * j + 1] * bb[8 * i + 2 * j + 1], hi[j], lo[j]);
+        *reinterpret_cast<uint4*>(st + St::TH + piece16(lane, i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(st + St::TL + piece16(lane, i)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
     __syncwarp();
@@ -371,15 +417,20 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
     const uint32_t sst = base + (c % NST) * St::BYTES;
     // Y = S K^T (both terms of S), Z = S Q^T (the first term)
     float y[2][4] = {}, yl[2][4] = {}, z[2][4] = {};
+    uint32_t kf[2][4], qf[2][4];
+    ldmatrix_x4(kf[0], sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, mi >> 1));
+    ldmatrix_x4(qf[0], sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, mi >> 1));
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t ah[4], al[4], kf[4], qf[4];
+      if (ks + 1 < D / 16) {
+        ldmatrix_x4(kf[(ks + 1) & 1], sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + 2 + (mi >> 1)));
+        ldmatrix_x4(qf[(ks + 1) & 1], sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + 2 + (mi >> 1)));
+      }
+      uint32_t ah[4], al[4];
       split_a<T>(S[2 * ks], S[2 * ks + 1], ah, al);
-      ldmatrix_x4(kf, sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
-      ldmatrix_x4(qf, sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
-      mma2<T>(y[0], y[1], ah, kf, 0, 2, 1, 3);
-      mma2<T>(yl[0], yl[1], al, kf, 0, 2, 1, 3);
-      mma2<T>(z[0], z[1], ah, qf, 0, 2, 1, 3);
+      mma2<T>(y[0], y[1], ah, kf[ks & 1], 0, 2, 1, 3);
+      mma2<T>(yl[0], yl[1], al, kf[ks & 1], 0, 2, 1, 3);
+      mma2<T>(z[0], z[1], ah, qf[ks & 1], 0, 2, 1, 3);
     }
     // W = V^T - Y diag(e^gam)
     uint32_t vf[4], wh[4], wl[4];
@@ -411,7 +462,7 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
       mma2<T>(ul[0], ul[1], wl, th, 0, 2, 1, 3);
       mma2<T>(ul[0], ul[1], wh, tl, 0, 2, 1, 3);
     }
-    uint32_t uh[4], dh[4], dl[4];
+    uint32_t uh[4], uo[4], dh[4], dl[4];
     {
       float dd[2][4];
 #pragma unroll
@@ -419,13 +470,12 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
         const float2 e = *reinterpret_cast<const float2*>(st + St::DEC + (8 * i + 2 * cq) * 4);
 #pragma unroll
         for (int j = 0; j < 4; ++j) u[i][j] += ul[i][j];
-        uh[2 * i] = F16<T>::pack(u[i][0], u[i][1]);
-        uh[2 * i + 1] = F16<T>::pack(u[i][2], u[i][3]);
         dd[i][0] = u[i][0] * e.x;
         dd[i][1] = u[i][1] * e.y;
         dd[i][2] = u[i][2] * e.x;
         dd[i][3] = u[i][3] * e.y;
       }
+      split_a<T>(u[0], u[1], uh, uo);
       split_a<T>(dd[0], dd[1], dh, dl);
     }
     // S <- e^gam_last S + U diag(dec) K
@@ -436,16 +486,19 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
       for (int e = 0; e < 4; ++e) S[j][e] *= gl;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t kf[4];
-      ldmatrix_x4_trans(kf, sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
-      mma2<T>(S[2 * ks], S[2 * ks + 1], dh, kf, 0, 1, 2, 3);
-      mma2<T>(S[2 * ks], S[2 * ks + 1], dl, kf, 0, 1, 2, 3);
+      uint32_t kt[4];
+      ldmatrix_x4_trans(kt, sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
+      mma2<T>(S[2 * ks], S[2 * ks + 1], dh, kt, 0, 1, 2, 3);
+      mma2<T>(S[2 * ks], S[2 * ks + 1], dl, kt, 0, 1, 2, 3);
     }
     // O = Z diag(e^gam) + U M^T, written token-major
     {
-      uint32_t mf[4];
-      ldmatrix_x4(mf, sst + St::M + piece16((mi & 1) * 8 + lr, mi >> 1));
-      mma2<T>(z[0], z[1], uh, mf, 0, 2, 1, 3);
+      uint32_t mh[4], ml[4];
+      ldmatrix_x4(mh, sst + St::MH + piece16((mi & 1) * 8 + lr, mi >> 1));
+      ldmatrix_x4(ml, sst + St::ML + piece16((mi & 1) * 8 + lr, mi >> 1));
+      mma2<T>(z[0], z[1], uh, mh, 0, 2, 1, 3);
+      mma2<T>(z[0], z[1], uo, mh, 0, 2, 1, 3);
+      mma2<T>(z[0], z[1], uh, ml, 0, 2, 1, 3);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[c % NST]);
