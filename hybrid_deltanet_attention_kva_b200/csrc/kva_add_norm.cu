@@ -48,36 +48,61 @@ __device__ __forceinline__ uint32_t q8_code(float y, float inv) {
   return static_cast<uint32_t>(static_cast<int>(c)) & 0xffu;
 }
 
-// One block of 256 threads per row.
-template <typename TX, typename TH, typename TO>
+// TPR threads (a warp, or a block of 256) take a row: NV groups of 4 values each, held in registers
+// from the one read of x and h to the last write.  Bandwidth-bound.
+template <typename TX, typename TH, typename TO, int TPR, int NV>
 __global__ void __launch_bounds__(256)
     add_rmsnorm_kernel(const TX* __restrict__ x, int64_t ldx, const TH* h, TH* h_out, int64_t ldh,
                        const float* __restrict__ g, TO* __restrict__ out, int64_t ldo,
                        __half* __restrict__ scales, int rows, int n, float eps) {
+  constexpr int RPB = 256 / TPR;  // rows a block
   griddep_wait_and_release();
-  const int64_t row = blockIdx.x;
-  float ss = 0.f;
-  for (int i = threadIdx.x * 4; i < n; i += 1024) {
-    const float4 a = Io<TX>::load(x + row * ldx + i), b = Io<TH>::load(h + row * ldh + i);
-    const float4 v = Io<TH>::store(h_out + row * ldh + i, make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w));
-    ss += v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
-  }
-  __shared__ float red[8];
-  ss = warp_sum(ss);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
-  __syncthreads();
-  float tot = 0.f;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / TPR;
+  const int col = threadIdx.x % TPR * 4;
+  if (TPR == 32 && row >= rows) return;  // (whole warps)
+  x += row * ldx;
+  h += row * ldh;
+  h_out += row * ldh;
+  out += row * ldo;
+  float4 v[NV], a[NV];
 #pragma unroll
-  for (int w = 0; w < 8; ++w) tot += red[w];
-  const float sc = rsqrtf(tot / static_cast<float>(n) + eps);
-  for (int i0 = 0; i0 < n; i0 += 1024) {  // (all threads: the 8 of a q8_0 block take part together)
-    const int i = i0 + threadIdx.x * 4;
+  for (int k = 0; k < NV; ++k) {
+    const int i = col + k * 4 * TPR;
+    v[k] = a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n) {
+      a[k] = Io<TX>::load(x + i);
+      v[k] = Io<TH>::load(h + i);
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = col + k * 4 * TPR;
+    if (i < n) {
+      v[k] = Io<TH>::store(h_out + i, make_float4(a[k].x + v[k].x, a[k].y + v[k].y, a[k].z + v[k].z, a[k].w + v[k].w));
+      ss += v[k].x * v[k].x + v[k].y * v[k].y + v[k].z * v[k].z + v[k].w * v[k].w;
+    }
+  }
+  ss = warp_sum(ss);
+  if (TPR > 32) {
+    __shared__ float red[8];
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
+    __syncthreads();
+    ss = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) ss += red[w];
+  }
+  const float sc = rsqrtf(ss / static_cast<float>(n) + eps);
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = col + k * 4 * TPR;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     if (i < n) {
-      const float4 v = Io<TH>::load(h_out + row * ldh + i), gg = *reinterpret_cast<const float4*>(g + i);
-      y = make_float4(v.x * sc * gg.x, v.y * sc * gg.y, v.z * sc * gg.z, v.w * sc * gg.w);
+      const float4 gg = *reinterpret_cast<const float4*>(g + i);
+      y = make_float4(v[k].x * sc * gg.x, v[k].y * sc * gg.y, v[k].z * sc * gg.z, v[k].w * sc * gg.w);
     }
     if constexpr (sizeof(TO) == 1) {
+      if (k * 4 * TPR >= n) break;  // (the same for every thread)
       float amax = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
       // a NaN or infinity makes the sum of 0 * y a NaN
       float bad = 0.f * y.x + 0.f * y.y + 0.f * y.z + 0.f * y.w;
@@ -93,12 +118,12 @@ __global__ void __launch_bounds__(256)
         uint32_t c = 0;
         if (fine)
           c = q8_code(y.x, inv) | q8_code(y.y, inv) << 8 | q8_code(y.z, inv) << 16 | q8_code(y.w, inv) << 24;
-        *reinterpret_cast<uint32_t*>(out + row * ldo + i) = c;
+        *reinterpret_cast<uint32_t*>(out + i) = c;
         if ((threadIdx.x & 7) == 0)
           scales[static_cast<int64_t>(i >> 5) * rows + row] = __float2half_rn(fine ? d : __int_as_float(0x7fffffff));
       }
     } else if (i < n) {
-      Io<TO>::store(out + row * ldo + i, y);
+      Io<TO>::store(out + i, y);
     }
   }
 }
@@ -118,11 +143,17 @@ struct Args {
   cudaStream_t s;
 };
 
-template <typename TX, typename TH, typename TO>
+template <typename TX, typename TH, typename TO, int TPR, int NV>
 cudaError_t launch(const Args& a) {
-  return launch_pdl(add_rmsnorm_kernel<TX, TH, TO>, dim3(a.rows), dim3(256), 0, a.s,
+  constexpr int RPB = 256 / TPR;
+  return launch_pdl(add_rmsnorm_kernel<TX, TH, TO, TPR, NV>, dim3((a.rows + RPB - 1) / RPB), dim3(256), 0, a.s,
                     static_cast<const TX*>(a.x), a.ldx, static_cast<const TH*>(a.h), static_cast<TH*>(a.h_out), a.ldh,
                     a.g, static_cast<TO*>(a.out), a.ldo, static_cast<__half*>(a.scales), a.rows, a.n, a.eps);
+}
+template <typename TX, typename TH, typename TO>
+cudaError_t launch(const Args& a) {
+  if (a.n <= 1024) return launch<TX, TH, TO, 32, 8>(a);
+  return a.n <= 8192 ? launch<TX, TH, TO, 256, 8>(a) : launch<TX, TH, TO, 256, 16>(a);
 }
 template <typename TX, typename TH>
 cudaError_t by_out(const Args& a, int out_dtype) {

@@ -1,19 +1,24 @@
-// Scores of rows of logits (kva_op_token_logprobs): with m = max x, s = sum e^(x-m) and
-// w = sum e^(x-m) (x-m),
-//     lse = m + log s,   log p_j = (x_j - m) - log s,   entropy = log s - w / s,
+// Scores of rows of logits (kva_op_token_logprobs): with a reference m, s = sum 2^((x-m) log2 e)
+// and w = sum 2^t t over t = (x-m) log2 e,
+//     lse = m + log s,   log p_j = (x_j - m) - log s,   entropy = ln 2 (log2 s - w / s),
 // and the n_top largest logits (ties in token order).
+//
+// One pass over the row: a thread keeps its own running maximum (its m), s and w.  The n_top
+// largest come from a second look at a few threads' pieces only: the n_top-th largest of 64
+// thread groups' maxima is a lower bound of the n_top-th largest logit, and about n_top (1 + n_top /
+// 128) logits reach it.  HBM is what bounds it when there are many rows; per logit the pass issues
+// one conversion, half a maximum, one multiply-add, clamp, exponential, sum and multiply-add.
 #include "../../include/kva_ops.h"
 #include "kva_common.cuh"
 
 namespace kva {
 namespace {
 
-constexpr int LP_THREADS = 512;
-
-template <typename T>
-__device__ __forceinline__ float lp_load(const T* p) { return F16<T>::to(*p); }
-template <>
-__device__ __forceinline__ float lp_load<float>(const float* p) { return *p; }
+constexpr int GROUPS = 64;      // thread groups whose maxima bound the alternatives
+constexpr int CAP = 1024;       // logits at or above the bound that are kept for ranking
+constexpr int MAX_CLUSTER = 8;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float T_MIN = -150.f; // 2^t is 0 from here on (and t times it: no 0 x infinity)
 
 struct LpArgs {
   const void* logits;
@@ -28,121 +33,424 @@ struct LpArgs {
   float* top_logprob;
 };
 
-// One block per row; one pass for the maximum, one for the sums, one per alternative.
+__device__ __forceinline__ float f_inf() { return __int_as_float(0x7f800000); }
+__device__ __forceinline__ float f_nan() { return __int_as_float(0x7fffffff); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// 16 bytes of logits
 template <typename T>
-__global__ void __launch_bounds__(LP_THREADS) logprobs_kernel(const LpArgs p) {
-  __shared__ float ra[LP_THREADS / 32], rb[LP_THREADS / 32];
-  __shared__ int ri[LP_THREADS / 32];
-  griddep_wait_and_release();
+struct Piece16 {
+  static constexpr int N = 8;
+  __device__ static __forceinline__ void unpack(const uint4& u, float (&f)[N]) {
+    const float2 a = F16<T>::unpack(u.x), b = F16<T>::unpack(u.y), c = F16<T>::unpack(u.z), d = F16<T>::unpack(u.w);
+    f[0] = a.x;
+    f[1] = a.y;
+    f[2] = b.x;
+    f[3] = b.y;
+    f[4] = c.x;
+    f[5] = c.y;
+    f[6] = d.x;
+    f[7] = d.y;
+  }
+};
+template <typename T>
+struct Piece;
+template <>
+struct Piece<__half> : Piece16<__half> {
+  static constexpr uint32_t NEG = 0xFC00FC00u;  // -infinity
+  __device__ static __forceinline__ float one(const __half* p) { return __half2float(*p); }
+  __device__ static __forceinline__ float largest(const uint4& u) {
+    const __half2* h = reinterpret_cast<const __half2*>(&u);
+    const __half2 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+    return max_nan(__low2float(m), __high2float(m));
+  }
+};
+template <>
+struct Piece<__nv_bfloat16> : Piece16<__nv_bfloat16> {
+  static constexpr uint32_t NEG = 0xFF80FF80u;
+  __device__ static __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  __device__ static __forceinline__ float largest(const uint4& u) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+    return max_nan(__low2float(m), __high2float(m));
+  }
+};
+template <>
+struct Piece<float> {
+  static constexpr int N = 4;
+  static constexpr uint32_t NEG = 0xFF800000u;
+  __device__ static __forceinline__ float one(const float* p) { return *p; }
+  __device__ static __forceinline__ void unpack(const uint4& u, float (&f)[N]) {
+    f[0] = __uint_as_float(u.x);
+    f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z);
+    f[3] = __uint_as_float(u.w);
+  }
+  __device__ static __forceinline__ float largest(const uint4& u) {
+    return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)),
+                   max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
+  }
+};
+
+// Running sums of a thread relative to 2^r, r = m log2 e rounded (r, not m, is the reference, so
+// its rounding costs nothing).  From 1e38 on m log2 e would overflow; there no two different floats
+// are near enough to weigh together: t = x - m is 0 or far below T_MIN.
+struct Sums {
+  float m, r, l, s, w;
+  __device__ __forceinline__ void init() {
+    m = -f_inf();
+    r = 0.f;
+    l = LOG2E;
+    s = w = 0.f;
+  }
+  __device__ __forceinline__ void rebase(float to) {
+    const float ln = fabsf(to) > 1e38f ? 1.f : LOG2E, rn = to * ln;
+    if (s > 0.f) {
+      const float d = l == LOG2E && ln == LOG2E ? fmaxf(r - rn, T_MIN) : T_MIN, f = ex2(d);
+      w = f * fmaf(d, s, w);
+      s *= f;
+    }
+    m = to;
+    r = rn;
+    l = ln;
+  }
+  __device__ __forceinline__ void add(float x) {
+    const float t = fmaxf(fmaf(x, l, -r), T_MIN), e = ex2(t);
+    s += e;
+    w = fmaf(e, t, w);
+  }
+};
+
+// one row's results, of a block or of the whole cluster
+struct RowOut {
+  float m, r, s, w;
+  int bad;
+};
+// a joined with b, in place of a
+__device__ __forceinline__ void join(RowOut& a, const RowOut& b) {
+  a.bad |= b.bad;
+  if (!(b.s > 0.f)) return;
+  if (!(a.s > 0.f)) {
+    const int bad = a.bad;
+    a = b;
+    a.bad = bad;
+    return;
+  }
+  RowOut hi = a.m >= b.m ? a : b, lo = a.m >= b.m ? b : a;
+  float d = fmaxf(lo.r - hi.r, T_MIN);
+  if (fabsf(hi.m) > 1e38f || fabsf(lo.m) > 1e38f) d = lo.m == hi.m ? 0.f : T_MIN;
+  const float f = ex2(d);
+  a.w = fmaf(f, fmaf(d, lo.s, lo.w), hi.w);
+  a.s = fmaf(f, lo.s, hi.s);
+  a.m = hi.m;
+  a.r = hi.r;
+}
+
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// candidate (v, i) comes before (ov, oi)
+__device__ __forceinline__ bool before(float v, int i, float ov, int oi) { return v > ov || (v == ov && i < oi); }
+
+// A cluster of CTAs per row, one contiguous range of 16-byte pieces each; block rank 0 joins them.
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const LpArgs p) {
+  using P = Piece<T>;
+  constexpr int WARPS = THREADS / 32, LANES = THREADS / GROUPS, BATCH = 4;
+  __shared__ RowOut part[WARPS], mine;
+  __shared__ float gmax[GROUPS], tau_s;
+  __shared__ float cv[CAP];
+  __shared__ int ci[CAP];
+  __shared__ float tv[KVA_LOGPROB_MAX_TOP];
+  __shared__ int ti[KVA_LOGPROB_MAX_TOP], n_cand;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cl = static_cast<int>(gridDim.y), rank = blockIdx.y;
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(p.logits) + row * p.ld;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const float kInf = __int_as_float(0x7f800000);
-  const float kNan = __int_as_float(0x7fffffff);
-
-  float m = -kInf, bad = 0.f;
-  for (int i = tid; i < p.V; i += LP_THREADS) {
-    const float v = lp_load(x + i);
-    m = fmaxf(m, v);
-    if (!(v < kInf)) bad = 1.f;  // NaN or +infinity
+  // pieces: 16-byte aligned; piece j holds logits j N - off ..; the first and the last may be partial
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+  const int np = static_cast<int>((static_cast<int64_t>(p.V) + off + P::N - 1) / P::N);
+  const int per = (np + cl - 1) / cl;
+  const int j0 = min(rank * per, np), j1 = min(j0 + per, np);
+  const int f0 = max(j0, off ? 1 : 0), f1 = min(j1, static_cast<int>((static_cast<int64_t>(p.V) + off) / P::N));
+  const uint4* xp = reinterpret_cast<const uint4*>(x - off);
+  if (tid == 0) {
+    n_cand = 0;
+    tau_s = -f_inf();
   }
+  griddep_wait_and_release();
+
+  Sums a;
+  a.init();
+  bool bad = false;
+  float x_tok = 0.f;
+  int tok = -1;
+  if (tid == 0 && rank == 0 && p.tokens) {
+    tok = p.tokens[row];
+    if (tok >= 0 && tok < p.V) x_tok = P::one(x + tok);
+  }
+  for (int j = f0 + tid; j < f1; j += BATCH * THREADS) {
+    uint4 u[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      u[i] = j + i * THREADS < f1 ? __ldcs(xp + j + i * THREADS) : make_uint4(P::NEG, P::NEG, P::NEG, P::NEG);
+    float cm = P::largest(u[0]);
+#pragma unroll
+    for (int i = 1; i < BATCH; ++i) cm = max_nan(cm, P::largest(u[i]));
+    if (!(cm <= a.m)) {
+      if (!(cm < f_inf())) {  // NaN or +infinity
+        bad = true;
+        break;
+      }
+      a.rebase(cm);
+    }
+    if (cm == -f_inf()) continue;
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      float f[P::N];
+      P::unpack(u[i], f);
+#pragma unroll
+      for (int e = 0; e < P::N; ++e) a.add(f[e]);
+    }
+  }
+  // the partial pieces: at most N - 1 logits before the first full one and after the last, a thread each
+  auto edge = [&](int e) {  // index of this thread's edge logit e, or -1
+    if (tid == 0 && rank == 0 && off) return e < min(P::N - off, p.V) ? e : -1;
+    const int last = static_cast<int>((static_cast<int64_t>(p.V) + off) / P::N) * P::N - off;  // behind the full pieces
+    if (tid == 1 && j1 == np && j0 < np && last >= (off ? P::N - off : 0)) return last + e < p.V ? last + e : -1;
+    return -1;
+  };
+  if (tid < 2)
+    for (int e = 0; e < P::N; ++e) {
+      const int i = edge(e);
+      if (i < 0) continue;
+      const float v = P::one(x + i);
+      if (!(v < f_inf())) bad = true;
+      else if (v > a.m) a.rebase(v);
+      if (!bad && v > -f_inf()) a.add(v);
+    }
+
+  // join the block's threads
+  float g = a.m;
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+  if (tid % LANES == 0) gmax[tid / LANES] = g;
+  RowOut ro{a.m, a.r, a.s, a.w, bad};
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    bad = fmaxf(bad, __shfl_xor_sync(0xffffffffu, bad, o));
+    RowOut b;
+    b.m = __shfl_xor_sync(0xffffffffu, ro.m, o);
+    b.r = __shfl_xor_sync(0xffffffffu, ro.r, o);
+    b.s = __shfl_xor_sync(0xffffffffu, ro.s, o);
+    b.w = __shfl_xor_sync(0xffffffffu, ro.w, o);
+    b.bad = __shfl_xor_sync(0xffffffffu, ro.bad, o);
+    join(ro, b);
   }
-  if (lane == 0) {
-    ra[warp] = m;
-    rb[warp] = bad;
-  }
+  if (lane == 0) part[warp] = ro;
   __syncthreads();
-  for (int i = 0; i < LP_THREADS / 32; ++i) {
-    m = fmaxf(m, ra[i]);
-    bad = fmaxf(bad, rb[i]);
-  }
-  __syncthreads();
-  const bool nan = bad != 0.f, empty = !nan && m == -kInf;
-
-  float s = 0.f, w = 0.f;
-  if (!nan && !empty)
-    for (int i = tid; i < p.V; i += LP_THREADS) {
-      const float d = lp_load(x + i) - m, e = expf(d);
-      s += e;
-      w += e > 0.f ? e * d : 0.f;
+  const int k = p.n_top;
+  if (k > 0) {
+    if (tid < GROUPS) {  // the k-th largest of the groups' maxima
+      const float v = gmax[tid];
+      int before_me = 0;
+#pragma unroll 8
+      for (int i = 0; i < GROUPS; ++i) before_me += before(gmax[i], i, v, tid);
+      if (before_me == k - 1) tau_s = v;
     }
-  s = warp_sum(s);
-  w = warp_sum(w);
-  if (lane == 0) {
-    ra[warp] = s;
-    rb[warp] = w;
-  }
-  __syncthreads();
-  s = w = 0.f;
-  for (int i = 0; i < LP_THREADS / 32; ++i) {
-    s += ra[i];
-    w += rb[i];
-  }
-  __syncthreads();
-  // a row with nothing left: with reference 0 and sum 1, x - m - log s is -infinity by itself
-  if (empty) {
-    m = w = 0.f;
-    s = 1.f;
-  }
-  const float logs = logf(s);
-  if (tid == 0) {
-    if (p.lse) p.lse[row] = nan ? kNan : empty ? -kInf : m + logs;
-    if (p.entropy) p.entropy[row] = nan ? kNan : logs - w / s;
-    if (p.tokens) {
-      const int t = p.tokens[row];
-      if (nan || t < -1 || t >= p.V) p.logprob[row] = kNan;
-      else if (t == -1) p.logprob[row] = 0.f;
-      else p.logprob[row] = (lp_load(x + t) - m) - logs;
-    }
-  }
-
-  // alternatives in order: the largest (value, then lowest id) behind the previous one
-  float pv = kInf;
-  int pi = -1;
-  for (int j = 0; j < p.n_top; ++j) {
-    float bv = -kInf;
-    int bi = -1;
-    if (!nan && !empty && (j == 0 || pi >= 0))
-      for (int i = tid; i < p.V; i += LP_THREADS) {
-        const float v = lp_load(x + i);
-        if (v > bv && (v < pv || (v == pv && i > pi))) {
-          bv = v;
-          bi = i;
+    __syncthreads();
+    const float tau = tau_s;
+    auto take = [&](float v, int i) {
+      if (v >= tau && v > -f_inf()) {
+        const int at = atomicAdd(&n_cand, 1);  // (the order does not matter: candidates are ranked)
+        if (at < CAP) {
+          cv[at] = v;
+          ci[at] = i;
         }
       }
+    };
+    // a warp looks again at the pieces of each of its threads that reach the bound
+    uint32_t again = __ballot_sync(0xffffffffu, a.m >= tau && a.m > -f_inf());
+    while (again) {
+      const int t = __ffs(again) - 1;
+      again &= again - 1;
+      for (int j = f0 + 32 * warp + t + lane * THREADS; j < f1; j += 32 * THREADS) {
+        const uint4 u = xp[j];
+        if (P::largest(u) >= tau) {
+          float f[P::N];
+          P::unpack(u, f);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-      const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-      if (oi >= 0 && (bi < 0 || ov > bv || (ov == bv && oi < bi))) {
-        bv = ov;
-        bi = oi;
+          for (int e = 0; e < P::N; ++e) take(f[e], j * P::N - off + e);
+        }
       }
     }
-    if (lane == 0) {
-      ra[warp] = bv;
-      ri[warp] = bi;
+    if (tid < 2)
+      for (int e = 0; e < P::N; ++e) {
+        const int i = edge(e);
+        if (i >= 0) take(P::one(x + i), i);
+      }
+    if (tid < k) {
+      tv[tid] = -f_inf();
+      ti[tid] = -1;
     }
     __syncthreads();
-    bv = ra[0];
-    bi = ri[0];
-    for (int i = 1; i < LP_THREADS / 32; ++i)
-      if (ri[i] >= 0 && (bi < 0 || ra[i] > bv || (ra[i] == bv && ri[i] < bi))) {
-        bv = ra[i];
-        bi = ri[i];
+    const int n = n_cand;
+    if (n <= CAP) {
+      for (int c = tid; c < n; c += THREADS) {
+        const float v = cv[c];
+        const int id = ci[c];
+        int before_me = 0;
+        for (int i = 0; i < n; ++i) before_me += before(cv[i], ci[i], v, id);
+        if (before_me < k) {
+          tv[before_me] = v;
+          ti[before_me] = id;
+        }
       }
-    __syncthreads();
-    pv = bv;
-    pi = bi;
-    if (tid == 0) {
-      p.top_id[row * p.n_top + j] = bi;
-      p.top_logprob[row * p.n_top + j] = nan ? kNan : bi < 0 ? -kInf : (bv - m) - logs;
+    } else {
+      // over CAP logits tie around the bound: one scan of the range per alternative, each for the
+      // first (value, token) behind the one before
+      const int e0 = max(j0 * P::N - off, 0), e1 = min(j1 * P::N - off, p.V);
+      float pv = f_inf();
+      int pi = -1;
+      for (int r = 0; r < k; ++r) {
+        float bv = -f_inf();
+        int bi = -1;
+        for (int i = e0 + tid; i < e1; i += THREADS) {
+          const float v = P::one(x + i);
+          if (v > bv && before(pv, pi, v, i)) {
+            bv = v;
+            bi = i;
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
+          const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
+          if (oi >= 0 && (bi < 0 || before(ov, oi, bv, bi))) {
+            bv = ov;
+            bi = oi;
+          }
+        }
+        if (lane == 0) {
+          cv[warp] = bv;
+          ci[warp] = bi;
+        }
+        __syncthreads();
+        bv = cv[0];
+        bi = ci[0];
+        for (int i = 1; i < WARPS; ++i)
+          if (ci[i] >= 0 && (bi < 0 || before(cv[i], ci[i], bv, bi))) {
+            bv = cv[i];
+            bi = ci[i];
+          }
+        __syncthreads();
+        pv = bv;
+        pi = bi;
+        if (tid == 0) {
+          tv[r] = bv;
+          ti[r] = bi;
+        }
+        if (bi < 0) break;  // (the same for every thread)
+      }
     }
   }
+  if (tid == 0) {
+    RowOut r = part[0];
+    for (int i = 1; i < WARPS; ++i) join(r, part[i]);
+    mine = r;
+  }
+  __syncthreads();
+  if (cl > 1) {
+    cluster_sync();
+    if (rank == 0) {
+      if (tid == 0) {
+        RowOut r = mine;
+        for (int c = 1; c < cl; ++c) {
+          const uint32_t at = mapa_shared(smem_u32(&mine), c);
+          RowOut b;
+          b.m = __uint_as_float(ld_cluster(at));
+          b.r = __uint_as_float(ld_cluster(at + 4));
+          b.s = __uint_as_float(ld_cluster(at + 8));
+          b.w = __uint_as_float(ld_cluster(at + 12));
+          b.bad = static_cast<int>(ld_cluster(at + 16));
+          join(r, b);
+        }
+        mine = r;
+      }
+      for (int c = tid; c < cl * k; c += THREADS) {  // at most 8 x 32 of CAP places
+        cv[c] = __uint_as_float(ld_cluster(mapa_shared(smem_u32(&tv[c % k]), c / k)));
+        ci[c] = static_cast<int>(ld_cluster(mapa_shared(smem_u32(&ti[c % k]), c / k)));
+      }
+      __syncthreads();
+      for (int c = tid; c < cl * k; c += THREADS) {
+        const float v = cv[c];
+        const int id = ci[c];
+        if (id < 0) continue;
+        int before_me = 0;
+        for (int i = 0; i < cl * k; ++i) before_me += ci[i] >= 0 && before(cv[i], ci[i], v, id);
+        if (before_me < k) {  // (rank 0's own list has been copied: its places are free)
+          tv[before_me] = v;
+          ti[before_me] = id;
+        }
+      }
+      __syncthreads();
+    }
+    cluster_sync();  // the other blocks' shared memory is read: they may end
+    if (rank != 0) return;
+  }
+  // a row with nothing left: with reference 0 and sum 1, x - m - log s is -infinity by itself
+  const bool nan = mine.bad != 0, empty = !nan && !(mine.s > 0.f);
+  const float m = empty ? 0.f : mine.m, s = empty ? 1.f : mine.s, w = empty ? 0.f : mine.w;
+  const float log2s = log2f(s);
+  // log sum e^(x-m): the reference 2^r is 2^(m log2 e) but for r's rounding, which is added back
+  const float logs = LN2 * (empty || fabsf(m) > 1e38f ? log2s : log2s - fmaf(m, LOG2E, -mine.r));
+  if (tid == 0) {
+    if (p.lse) p.lse[row] = nan ? f_nan() : empty ? -f_inf() : m + logs;
+    if (p.entropy) p.entropy[row] = nan ? f_nan() : LN2 * (log2s - w / s);
+    if (p.tokens) p.logprob[row] = nan || tok < -1 || tok >= p.V ? f_nan() : tok == -1 ? 0.f : (x_tok - m) - logs;
+  }
+  for (int r = tid; r < k; r += THREADS) {
+    p.top_id[row * k + r] = nan ? -1 : ti[r];
+    p.top_logprob[row * k + r] = nan ? f_nan() : (tv[r] - m) - logs;
+  }
+}
+
+// Blocks a row: as many as keep the GPU's SMs busy, at least one piece a thread and block, 8 at most
+template <typename T, int THREADS>
+cudaError_t launch(const LpArgs& p, int rows, cudaStream_t s) {
+  const int np = (p.V + Piece<T>::N - 1) / Piece<T>::N, sms = num_sms();
+  int cl = 1;
+  while (cl < MAX_CLUSTER && static_cast<int64_t>(rows) * cl < sms && np / (2 * cl) >= THREADS) cl *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(rows, cl);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = cl;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cl > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS>, p);
+}
+template <typename T>
+cudaError_t launch(const LpArgs& p, int rows, cudaStream_t s) {
+  // short rows take small blocks, so that a thread still has a batch of pieces
+  return (p.V + Piece<T>::N - 1) / Piece<T>::N <= 1024 ? launch<T, 128>(p, rows, s) : launch<T, 512>(p, rows, s);
 }
 
 }  // namespace
@@ -166,9 +474,8 @@ extern "C" int kva_op_token_logprobs(const void* logits, int32_t dtype, int64_t 
     return KVA_ERR_ALIGNMENT;
   const LpArgs p{logits, ld, n_vocab, tokens, logprob, lse, entropy, n_top, top_id, top_logprob};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid(rows), block(LP_THREADS);
-  const cudaError_t r = dtype == KVA_F32   ? launch_pdl(logprobs_kernel<float>, grid, block, 0, s, p)
-                        : dtype == KVA_F16 ? launch_pdl(logprobs_kernel<__half>, grid, block, 0, s, p)
-                                           : launch_pdl(logprobs_kernel<__nv_bfloat16>, grid, block, 0, s, p);
+  const cudaError_t r = dtype == KVA_F32   ? launch<float>(p, rows, s)
+                        : dtype == KVA_F16 ? launch<__half>(p, rows, s)
+                                           : launch<__nv_bfloat16>(p, rows, s);
   return r == cudaSuccess ? KVA_OK : KVA_ERR_CUDA;
 }
