@@ -41,21 +41,31 @@ struct Io<__half> : Io16<__half> {};
 template <>
 struct Io<__nv_bfloat16> : Io16<__nv_bfloat16> {};
 
-// One q8_0 code: round(y / d) half away from zero (y * inv within +-127 and finite)
-__device__ __forceinline__ uint32_t q8_code(float y, float inv) {
-  const float r = y * inv, t = truncf(r);
-  const float c = t + (fabsf(r - t) >= 0.5f ? copysignf(1.f, r) : 0.f);
-  return static_cast<uint32_t>(static_cast<int>(c)) & 0xffu;
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// One q8_0 code, round(r) half away from zero for |r| < 128, without the conversion unit (a quarter
+// of the other units' rate): |r| + 0.5 + 2^22 cut to steps of 0.5 holds floor(|r| + 0.5) above its
+// last mantissa bit.
+__device__ __forceinline__ uint32_t q8_code(float r) {
+  const uint32_t c = (__float_as_uint(__fadd_rz(fabsf(r), 4194304.5f)) >> 1) & 0x7fu;
+  const uint32_t s = static_cast<uint32_t>(__float_as_int(r) >> 31);
+  return (c ^ s) - s;
+}
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {  // low bytes
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// TPR threads (a warp, or a block of 256) take a row: NV groups of 4 values each, held in registers
+// TPR threads (a warp, or the block) take a row: NV groups of 4 values each, held in registers
 // from the one read of x and h to the last write.  Bandwidth-bound.
 template <typename TX, typename TH, typename TO, int TPR, int NV>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     add_rmsnorm_kernel(const TX* __restrict__ x, int64_t ldx, const TH* h, TH* h_out, int64_t ldh,
                        const float* __restrict__ g, TO* __restrict__ out, int64_t ldo,
                        __half* __restrict__ scales, int rows, int n, float eps) {
-  constexpr int RPB = 256 / TPR;  // rows a block
+  constexpr int THREADS = TPR < 256 ? 256 : TPR, RPB = THREADS / TPR;  // rows a block
   griddep_wait_and_release();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / TPR;
   const int col = threadIdx.x % TPR * 4;
@@ -85,12 +95,12 @@ __global__ void __launch_bounds__(256)
   }
   ss = warp_sum(ss);
   if (TPR > 32) {
-    __shared__ float red[8];
+    __shared__ float red[THREADS / 32];
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
     __syncthreads();
     ss = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) ss += red[w];
+    for (int w = 0; w < THREADS / 32; ++w) ss += red[w];
   }
   const float sc = rsqrtf(ss / static_cast<float>(n) + eps);
 #pragma unroll
@@ -103,21 +113,17 @@ __global__ void __launch_bounds__(256)
     }
     if constexpr (sizeof(TO) == 1) {
       if (k * 4 * TPR >= n) break;  // (the same for every thread)
-      float amax = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
-      // a NaN or infinity makes the sum of 0 * y a NaN
-      float bad = 0.f * y.x + 0.f * y.y + 0.f * y.z + 0.f * y.w;
+      float amax = max_nan(max_nan(fabsf(y.x), fabsf(y.y)), max_nan(fabsf(y.z), fabsf(y.w)));
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) {
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        bad += __shfl_xor_sync(0xffffffffu, bad, o);
-      }
+      for (int o = 4; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (i < n) {
-        const bool fine = bad == 0.f;
-        // (a subnormal d is 0 in fp16, whatever the codes; its reciprocal could overflow)
-        const float d = amax / 127.f, inv = fine && d >= 1.1754944e-38f ? 1.f / d : 0.f;
+        const bool fine = amax < __int_as_float(0x7f800000);
+        const float d = amax * (1.f / 127.f);
+        // 127 / max off by 2 ulp moves a code only where y / d is that near to a half.  (From a
+        // subnormal d the reciprocal could overflow; such a d is 0 in fp16, whatever the codes.)
+        const float inv = fine && d >= 1.1754944e-38f ? __fdividef(127.f, amax) : 0.f;
         uint32_t c = 0;
-        if (fine)
-          c = q8_code(y.x, inv) | q8_code(y.y, inv) << 8 | q8_code(y.z, inv) << 16 | q8_code(y.w, inv) << 24;
+        if (fine) c = pack4(q8_code(y.x * inv), q8_code(y.y * inv), q8_code(y.z * inv), q8_code(y.w * inv));
         *reinterpret_cast<uint32_t*>(out + i) = c;
         if ((threadIdx.x & 7) == 0)
           scales[static_cast<int64_t>(i >> 5) * rows + row] = __float2half_rn(fine ? d : __int_as_float(0x7fffffff));
@@ -145,15 +151,17 @@ struct Args {
 
 template <typename TX, typename TH, typename TO, int TPR, int NV>
 cudaError_t launch(const Args& a) {
-  constexpr int RPB = 256 / TPR;
-  return launch_pdl(add_rmsnorm_kernel<TX, TH, TO, TPR, NV>, dim3((a.rows + RPB - 1) / RPB), dim3(256), 0, a.s,
+  constexpr int THREADS = TPR < 256 ? 256 : TPR, RPB = THREADS / TPR;
+  return launch_pdl(add_rmsnorm_kernel<TX, TH, TO, TPR, NV>, dim3((a.rows + RPB - 1) / RPB), dim3(THREADS), 0, a.s,
                     static_cast<const TX*>(a.x), a.ldx, static_cast<const TH*>(a.h), static_cast<TH*>(a.h_out), a.ldh,
                     a.g, static_cast<TO*>(a.out), a.ldo, static_cast<__half*>(a.scales), a.rows, a.n, a.eps);
 }
 template <typename TX, typename TH, typename TO>
 cudaError_t launch(const Args& a) {
   if (a.n <= 1024) return launch<TX, TH, TO, 32, 8>(a);
-  return a.n <= 8192 ? launch<TX, TH, TO, 256, 8>(a) : launch<TX, TH, TO, 256, 16>(a);
+  if (a.n <= 4096) return launch<TX, TH, TO, 256, 4>(a);
+  if (a.n <= 6144) return launch<TX, TH, TO, 256, 6>(a);
+  return a.n <= 8192 ? launch<TX, TH, TO, 256, 8>(a) : launch<TX, TH, TO, 512, 8>(a);
 }
 template <typename TX, typename TH>
 cudaError_t by_out(const Args& a, int out_dtype) {

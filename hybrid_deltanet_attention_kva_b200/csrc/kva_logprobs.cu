@@ -3,7 +3,7 @@
 //     lse = m + log s,   log p_j = (x_j - m) - log s,   entropy = ln 2 (log2 s - w / s),
 // and the n_top largest logits (ties in token order).
 //
-// One pass over the row: a thread keeps its own running maximum (its m), s and w.  The n_top
+// One pass over the row: a thread keeps its own maximum, s and w.  The n_top
 // largest come from a second look at a few threads' pieces only: the n_top-th largest of 64
 // thread groups' maxima is a lower bound of the n_top-th largest logit, and about n_top (1 + n_top /
 // 128) logits reach it.  HBM is what bounds it when there are many rows; per logit the pass issues
@@ -44,6 +44,23 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
+}
+
+// two fp32 operations an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
 }
 
 // 16 bytes of logits
@@ -101,58 +118,89 @@ struct Piece<float> {
   }
 };
 
-// Running sums of a thread relative to 2^r, r = m log2 e rounded (r, not m, is the reference, so
-// its rounding costs nothing).  From 1e38 on m log2 e would overflow; there no two different floats
-// are near enough to weigh together: t = x - m is 0 or far below T_MIN.
+// Running sums of a thread relative to 2^r.  r follows the running maximum only when a logit comes
+// 2^16 above it (so t keeps 20 bits behind the point), so it is set by the first batch and hardly
+// ever again.  It is some logit times log2 e, rounded: r itself is the reference, so its rounding costs
+// nothing.  From 1e38 on m log2 e would overflow; there no two different floats are near enough to
+// weigh together: the factor is 1 and t = x - m is 0 or far below T_MIN.
+constexpr float REBASE = 16.f;
 struct Sums {
-  float m, r, l, s, w;
+  float m, r, l;      // largest logit so far; the reference and its factor
+  float2 s, w;        // two halves, for the packed fp32 instructions
   __device__ __forceinline__ void init() {
-    m = -f_inf();
-    r = 0.f;
+    m = r = -f_inf();
     l = LOG2E;
-    s = w = 0.f;
+    s = w = make_float2(0.f, 0.f);
   }
+  __device__ __forceinline__ bool huge() const { return l != LOG2E; }
   __device__ __forceinline__ void rebase(float to) {
     const float ln = fabsf(to) > 1e38f ? 1.f : LOG2E, rn = to * ln;
-    if (s > 0.f) {
-      const float d = l == LOG2E && ln == LOG2E ? fmaxf(r - rn, T_MIN) : T_MIN, f = ex2(d);
-      w = f * fmaf(d, s, w);
-      s *= f;
-    }
-    m = to;
+    const float d = l == LOG2E && ln == LOG2E ? fmaxf(r - rn, T_MIN) : T_MIN, f = ex2(d);
+    // (nothing to move from the first reference, -infinity: s and w are 0)
+    w = make_float2(f * fmaf(d, s.x, w.x), f * fmaf(d, s.y, w.y));
+    s = make_float2(f * s.x, f * s.y);
     r = rn;
     l = ln;
   }
-  __device__ __forceinline__ void add(float x) {
-    const float t = fmaxf(fmaf(x, l, -r), T_MIN), e = ex2(t);
-    s += e;
-    w = fmaf(e, t, w);
+  // takes a batch whose largest logit is cm; false: NaN or infinity, the row has no distribution
+  __device__ __forceinline__ bool take(float cm) {
+    if (!(fmaf(cm, l, -r) <= REBASE)) {
+      if (!(cm < f_inf())) return false;
+      if (cm > -f_inf()) rebase(cm);
+    }
+    m = fmaxf(m, cm);
+    return true;
+  }
+  // two logits; T_MIN keeps -infinity (0 x infinity) out of w
+  __device__ __forceinline__ void add(float2 x) {
+    float2 t = fma2(x, make_float2(l, l), make_float2(-r, -r));
+    t = make_float2(fmaxf(t.x, T_MIN), fmaxf(t.y, T_MIN));
+    const float2 e = make_float2(ex2(t.x), ex2(t.y));
+    s = add2(s, e);
+    w = fma2(e, t, w);
   }
 };
 
-// one row's results, of a block or of the whole cluster
+// a row's results so far: of a warp, a block or the cluster; s and w relative to 2^r (factor l)
 struct RowOut {
-  float m, r, s, w;
+  float m, r, l, s, w;
   int bad;
 };
-// a joined with b, in place of a
+// a joined with b, in place of a, relative to the reference of the larger maximum
 __device__ __forceinline__ void join(RowOut& a, const RowOut& b) {
-  a.bad |= b.bad;
-  if (!(b.s > 0.f)) return;
-  if (!(a.s > 0.f)) {
-    const int bad = a.bad;
-    a = b;
-    a.bad = bad;
-    return;
+  const int bad = a.bad | b.bad;
+  if (b.s > 0.f) {
+    if (!(a.s > 0.f)) {
+      a = b;
+    } else {
+      const RowOut hi = a.m >= b.m ? a : b, lo = a.m >= b.m ? b : a;
+      const float d = lo.l == LOG2E && hi.l == LOG2E ? fmaxf(lo.r - hi.r, T_MIN)
+                                                     : lo.l == hi.l && lo.r == hi.r ? 0.f : T_MIN;
+      const float f = ex2(d);
+      a.w = fmaf(f, fmaf(d, lo.s, lo.w), hi.w);
+      a.s = fmaf(f, lo.s, hi.s);
+      a.m = hi.m;
+      a.r = hi.r;
+      a.l = hi.l;
+    }
   }
-  RowOut hi = a.m >= b.m ? a : b, lo = a.m >= b.m ? b : a;
-  float d = fmaxf(lo.r - hi.r, T_MIN);
-  if (fabsf(hi.m) > 1e38f || fabsf(lo.m) > 1e38f) d = lo.m == hi.m ? 0.f : T_MIN;
-  const float f = ex2(d);
-  a.w = fmaf(f, fmaf(d, lo.s, lo.w), hi.w);
-  a.s = fmaf(f, lo.s, hi.s);
-  a.m = hi.m;
-  a.r = hi.r;
+  a.bad = bad;
+}
+
+// over N lanes of every N-lane group
+template <int N>
+__device__ __forceinline__ void join_lanes(RowOut& a) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    RowOut b;
+    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+    b.r = __shfl_xor_sync(0xffffffffu, a.r, o);
+    b.l = __shfl_xor_sync(0xffffffffu, a.l, o);
+    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+    b.w = __shfl_xor_sync(0xffffffffu, a.w, o);
+    b.bad = __shfl_xor_sync(0xffffffffu, a.bad, o);
+    join(a, b);
+  }
 }
 
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
@@ -209,12 +257,9 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
     float cm = P::largest(u[0]);
 #pragma unroll
     for (int i = 1; i < BATCH; ++i) cm = max_nan(cm, P::largest(u[i]));
-    if (!(cm <= a.m)) {
-      if (!(cm < f_inf())) {  // NaN or +infinity
-        bad = true;
-        break;
-      }
-      a.rebase(cm);
+    if (!a.take(cm)) {
+      bad = true;
+      break;
     }
     if (cm == -f_inf()) continue;
 #pragma unroll
@@ -222,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
       float f[P::N];
       P::unpack(u[i], f);
 #pragma unroll
-      for (int e = 0; e < P::N; ++e) a.add(f[e]);
+      for (int e = 0; e < P::N; e += 2) a.add(make_float2(f[e], f[e + 1]));
     }
   }
   // the partial pieces: at most N - 1 logits before the first full one and after the last, a thread each
@@ -237,9 +282,8 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
       const int i = edge(e);
       if (i < 0) continue;
       const float v = P::one(x + i);
-      if (!(v < f_inf())) bad = true;
-      else if (v > a.m) a.rebase(v);
-      if (!bad && v > -f_inf()) a.add(v);
+      if (!a.take(v)) bad = true;
+      else if (v > -f_inf()) a.add(make_float2(v, -f_inf()));
     }
 
   // join the block's threads
@@ -247,27 +291,37 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
   if (tid % LANES == 0) gmax[tid / LANES] = g;
-  RowOut ro{a.m, a.r, a.s, a.w, bad};
+  // a warp's sums, relative to its largest logit
+  RowOut ro;
+  {
+    float m = a.m;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    RowOut b;
-    b.m = __shfl_xor_sync(0xffffffffu, ro.m, o);
-    b.r = __shfl_xor_sync(0xffffffffu, ro.r, o);
-    b.s = __shfl_xor_sync(0xffffffffu, ro.s, o);
-    b.w = __shfl_xor_sync(0xffffffffu, ro.w, o);
-    b.bad = __shfl_xor_sync(0xffffffffu, ro.bad, o);
-    join(ro, b);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float l = fabsf(m) > 1e38f ? 1.f : LOG2E, r = m * l;
+    const float sa = a.s.x + a.s.y, wa = a.w.x + a.w.y;
+    float d = a.l == LOG2E && l == LOG2E ? fmaxf(a.r - r, T_MIN) : a.l == l && a.r == r ? 0.f : T_MIN;
+    if (!(sa > 0.f)) d = T_MIN;
+    const float f = ex2(d);
+    ro.m = m;
+    ro.r = r;
+    ro.l = l;
+    ro.s = warp_sum(f * sa);
+    ro.w = warp_sum(f * fmaf(d, sa, wa));
+    ro.bad = __any_sync(0xffffffffu, bad);
   }
   if (lane == 0) part[warp] = ro;
   __syncthreads();
   const int k = p.n_top;
   if (k > 0) {
-    if (tid < GROUPS) {  // the k-th largest of the groups' maxima
-      const float v = gmax[tid];
+    {  // the k-th largest of the groups' maxima: each of a group's threads compares with a share of them
+      const int mg = tid / LANES, sub = tid % LANES;
+      const float v = gmax[mg];
       int before_me = 0;
-#pragma unroll 8
-      for (int i = 0; i < GROUPS; ++i) before_me += before(gmax[i], i, v, tid);
-      if (before_me == k - 1) tau_s = v;
+#pragma unroll
+      for (int i = 0; i < GROUPS / LANES; ++i) before_me += before(gmax[i * LANES + sub], i * LANES + sub, v, mg);
+#pragma unroll
+      for (int o = 1; o < LANES; o <<= 1) before_me += __shfl_xor_sync(0xffffffffu, before_me, o);
+      if (sub == 0 && before_me == k - 1) tau_s = v;
     }
     __syncthreads();
     const float tau = tau_s;
@@ -365,28 +419,29 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
       }
     }
   }
-  if (tid == 0) {
-    RowOut r = part[0];
-    for (int i = 1; i < WARPS; ++i) join(r, part[i]);
-    mine = r;
+  if (warp == 0) {
+    RowOut r = part[lane % WARPS];
+    join_lanes<WARPS>(r);
+    if (lane == 0) mine = r;
   }
   __syncthreads();
   if (cl > 1) {
     cluster_sync();
     if (rank == 0) {
-      if (tid == 0) {
-        RowOut r = mine;
-        for (int c = 1; c < cl; ++c) {
-          const uint32_t at = mapa_shared(smem_u32(&mine), c);
-          RowOut b;
-          b.m = __uint_as_float(ld_cluster(at));
-          b.r = __uint_as_float(ld_cluster(at + 4));
-          b.s = __uint_as_float(ld_cluster(at + 8));
-          b.w = __uint_as_float(ld_cluster(at + 12));
-          b.bad = static_cast<int>(ld_cluster(at + 16));
-          join(r, b);
+      if (warp == 0) {
+        RowOut r{-f_inf(), 0.f, LOG2E, 0.f, 0.f, 0};
+        if (lane < cl) {
+          const uint32_t at = mapa_shared(smem_u32(&mine), lane);
+          r.m = __uint_as_float(ld_cluster(at));
+          r.r = __uint_as_float(ld_cluster(at + 4));
+          r.l = __uint_as_float(ld_cluster(at + 8));
+          r.s = __uint_as_float(ld_cluster(at + 12));
+          r.w = __uint_as_float(ld_cluster(at + 16));
+          r.bad = static_cast<int>(ld_cluster(at + 20));
         }
-        mine = r;
+        join_lanes<MAX_CLUSTER>(r);
+        __syncwarp();
+        if (lane == 0) mine = r;
       }
       for (int c = tid; c < cl * k; c += THREADS) {  // at most 8 x 32 of CAP places
         cv[c] = __uint_as_float(ld_cluster(mapa_shared(smem_u32(&tv[c % k]), c / k)));
@@ -414,7 +469,7 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
   const float m = empty ? 0.f : mine.m, s = empty ? 1.f : mine.s, w = empty ? 0.f : mine.w;
   const float log2s = log2f(s);
   // log sum e^(x-m): the reference 2^r is 2^(m log2 e) but for r's rounding, which is added back
-  const float logs = LN2 * (empty || fabsf(m) > 1e38f ? log2s : log2s - fmaf(m, LOG2E, -mine.r));
+  const float logs = LN2 * (empty || mine.l != LOG2E ? log2s : log2s - fmaf(m, LOG2E, -mine.r));
   if (tid == 0) {
     if (p.lse) p.lse[row] = nan ? f_nan() : empty ? -f_inf() : m + logs;
     if (p.entropy) p.entropy[row] = nan ? f_nan() : LN2 * (log2s - w / s);
