@@ -203,26 +203,39 @@ __device__ __forceinline__ void join_lanes(RowOut& a) {
   }
 }
 
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
+// A logit and its token as one number: larger logits first, of equal ones the lower token.  0: none.
+__device__ __forceinline__ unsigned long long key_of(float v, int i) {
+  const uint32_t u = __float_as_uint(v + 0.f);  // (-0 is 0)
+  return static_cast<unsigned long long>(u & 0x80000000u ? ~u : u | 0x80000000u) << 32 | (0xffffffffu - i);
+}
+__device__ __forceinline__ float key_value(unsigned long long k) {
+  const uint32_t u = static_cast<uint32_t>(k >> 32);
+  return k ? __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u) : -f_inf();
+}
+__device__ __forceinline__ int key_token(unsigned long long k) {
+  return k ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)) : -1;
 }
 
-// candidate (v, i) comes before (ov, oi)
-__device__ __forceinline__ bool before(float v, int i, float ov, int oi) { return v > ov || (v == ov && i < oi); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
 
 // A cluster of CTAs per row, one contiguous range of 16-byte pieces each; block rank 0 joins them.
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const LpArgs p) {
   using P = Piece<T>;
   constexpr int WARPS = THREADS / 32, LANES = THREADS / GROUPS, BATCH = 4;
-  __shared__ RowOut part[WARPS], mine;
+  using Key = unsigned long long;
+  __shared__ RowOut part[WARPS], mine, all[MAX_CLUSTER];
   __shared__ float gmax[GROUPS], tau_s;
-  __shared__ float cv[CAP];
-  __shared__ int ci[CAP];
-  __shared__ float tv[KVA_LOGPROB_MAX_TOP];
-  __shared__ int ti[KVA_LOGPROB_MAX_TOP], n_cand;
+  __shared__ Key cand[CAP], top[KVA_LOGPROB_MAX_TOP], all_top[MAX_CLUSTER * KVA_LOGPROB_MAX_TOP];
+  __shared__ int n_cand, n_again;
+  __shared__ uint16_t again[THREADS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cl = static_cast<int>(gridDim.y), rank = blockIdx.y;
   const int64_t row = blockIdx.x;
@@ -235,9 +248,10 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
   const int f0 = max(j0, off ? 1 : 0), f1 = min(j1, static_cast<int>((static_cast<int64_t>(p.V) + off) / P::N));
   const uint4* xp = reinterpret_cast<const uint4*>(x - off);
   if (tid == 0) {
-    n_cand = 0;
+    n_cand = n_again = 0;
     tau_s = -f_inf();
   }
+  if (cl > 1) cluster_arrive();  // (waited for before the first write to another block)
   griddep_wait_and_release();
 
   Sums a;
@@ -253,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
     uint4 u[BATCH];
 #pragma unroll
     for (int i = 0; i < BATCH; ++i)
-      u[i] = j + i * THREADS < f1 ? __ldcs(xp + j + i * THREADS) : make_uint4(P::NEG, P::NEG, P::NEG, P::NEG);
+      u[i] = j + i * THREADS < f1 ? __ldg(xp + j + i * THREADS) : make_uint4(P::NEG, P::NEG, P::NEG, P::NEG);
     float cm = P::largest(u[0]);
 #pragma unroll
     for (int i = 1; i < BATCH; ++i) cm = max_nan(cm, P::largest(u[i]));
@@ -270,21 +284,23 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
       for (int e = 0; e < P::N; e += 2) a.add(make_float2(f[e], f[e + 1]));
     }
   }
-  // the partial pieces: at most N - 1 logits before the first full one and after the last, a thread each
-  auto edge = [&](int e) {  // index of this thread's edge logit e, or -1
-    if (tid == 0 && rank == 0 && off) return e < min(P::N - off, p.V) ? e : -1;
-    const int last = static_cast<int>((static_cast<int64_t>(p.V) + off) / P::N) * P::N - off;  // behind the full pieces
-    if (tid == 1 && j1 == np && j0 < np && last >= (off ? P::N - off : 0)) return last + e < p.V ? last + e : -1;
-    return -1;
-  };
-  if (tid < 2)
-    for (int e = 0; e < P::N; ++e) {
-      const int i = edge(e);
-      if (i < 0) continue;
-      const float v = P::one(x + i);
-      if (!a.take(v)) bad = true;
-      else if (v > -f_inf()) a.add(make_float2(v, -f_inf()));
+  // the partial pieces, at most N - 1 logits before the first full one and behind the last: a thread
+  // each.  e0 and e1 are the logits of this thread's
+  int e0 = 0, e1 = 0;
+  if (tid == 0 && rank == 0 && off) {
+    e1 = min(P::N - off, p.V);
+  } else if (tid == 1 && j1 == np && j0 < np) {
+    const int last = static_cast<int>((static_cast<int64_t>(p.V) + off) / P::N * P::N) - off;  // behind the full pieces
+    if (last >= (off ? P::N - off : 0)) {
+      e0 = last;
+      e1 = p.V;
     }
+  }
+  for (int i = e0; i < e1; ++i) {
+    const float v = P::one(x + i);
+    if (!a.take(v)) bad = true;
+    else if (v > -f_inf()) a.add(make_float2(v, -f_inf()));
+  }
 
   // join the block's threads
   float g = a.m;
@@ -312,35 +328,44 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
   if (lane == 0) part[warp] = ro;
   __syncthreads();
   const int k = p.n_top;
+  float tau = 0.f;
   if (k > 0) {
-    {  // the k-th largest of the groups' maxima: each of a group's threads compares with a share of them
-      const int mg = tid / LANES, sub = tid % LANES;
-      const float v = gmax[mg];
-      int before_me = 0;
+    // the k-th largest of the groups' maxima: each of a group's threads compares with a share of them
+    const int mg = tid / LANES, sub = tid % LANES;
+    const float v = gmax[mg];
+    int before_me = 0;
 #pragma unroll
-      for (int i = 0; i < GROUPS / LANES; ++i) before_me += before(gmax[i * LANES + sub], i * LANES + sub, v, mg);
-#pragma unroll
-      for (int o = 1; o < LANES; o <<= 1) before_me += __shfl_xor_sync(0xffffffffu, before_me, o);
-      if (sub == 0 && before_me == k - 1) tau_s = v;
+    for (int i = 0; i < GROUPS / LANES; ++i) {
+      const float o = gmax[i * LANES + sub];
+      before_me += o > v || (o == v && i * LANES + sub < mg);
     }
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) before_me += __shfl_xor_sync(0xffffffffu, before_me, o);
+    if (sub == 0 && before_me == k - 1) tau_s = v;
     __syncthreads();
-    const float tau = tau_s;
+    tau = tau_s;
+    if (tid < k) top[tid] = 0;
+    // the threads that reach the bound are looked at again, a warp for each (its lanes take the
+    // thread's pieces), so that one memory latency serves them all
+    if (a.m >= tau && a.m > -f_inf()) again[atomicAdd(&n_again, 1)] = static_cast<uint16_t>(tid);
+    __syncthreads();
+  }
+  if (warp == WARPS - 1) {
+    RowOut r = part[lane % WARPS];
+    join_lanes<WARPS>(r);
+    if (lane == 0) mine = r;
+  }
+  if (k > 0) {
     auto take = [&](float v, int i) {
       if (v >= tau && v > -f_inf()) {
         const int at = atomicAdd(&n_cand, 1);  // (the order does not matter: candidates are ranked)
-        if (at < CAP) {
-          cv[at] = v;
-          ci[at] = i;
-        }
+        if (at < CAP) cand[at] = key_of(v, i);
       }
     };
-    // a warp looks again at the pieces of each of its threads that reach the bound
-    uint32_t again = __ballot_sync(0xffffffffu, a.m >= tau && a.m > -f_inf());
-    while (again) {
-      const int t = __ffs(again) - 1;
-      again &= again - 1;
-      for (int j = f0 + 32 * warp + t + lane * THREADS; j < f1; j += 32 * THREADS) {
-        const uint4 u = xp[j];
+    const int n_look = n_again;
+    for (int c = warp; c < n_look; c += WARPS)
+      for (int j = f0 + again[c] + lane * THREADS; j < f1; j += 32 * THREADS) {
+        const uint4 u = __ldg(xp + j);
         if (P::largest(u) >= tau) {
           float f[P::N];
           P::unpack(u, f);
@@ -348,121 +373,73 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
           for (int e = 0; e < P::N; ++e) take(f[e], j * P::N - off + e);
         }
       }
-    }
-    if (tid < 2)
-      for (int e = 0; e < P::N; ++e) {
-        const int i = edge(e);
-        if (i >= 0) take(P::one(x + i), i);
-      }
-    if (tid < k) {
-      tv[tid] = -f_inf();
-      ti[tid] = -1;
-    }
+    for (int i = e0; i < e1; ++i) take(P::one(x + i), i);
     __syncthreads();
     const int n = n_cand;
     if (n <= CAP) {
       for (int c = tid; c < n; c += THREADS) {
-        const float v = cv[c];
-        const int id = ci[c];
+        const Key mk = cand[c];
         int before_me = 0;
-        for (int i = 0; i < n; ++i) before_me += before(cv[i], ci[i], v, id);
-        if (before_me < k) {
-          tv[before_me] = v;
-          ti[before_me] = id;
-        }
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) before_me += cand[i] > mk;
+        if (before_me < k) top[before_me] = mk;
       }
     } else {
       // over CAP logits tie around the bound: one scan of the range per alternative, each for the
-      // first (value, token) behind the one before
-      const int e0 = max(j0 * P::N - off, 0), e1 = min(j1 * P::N - off, p.V);
-      float pv = f_inf();
-      int pi = -1;
-      for (int r = 0; r < k; ++r) {
-        float bv = -f_inf();
-        int bi = -1;
-        for (int i = e0 + tid; i < e1; i += THREADS) {
+      // largest key below the one before
+      const int s0 = max(j0 * P::N - off, 0), s1 = static_cast<int>(min(static_cast<int64_t>(j1) * P::N - off, static_cast<int64_t>(p.V)));
+      Key prev = ~0ull;
+      for (int r = 0; r < k && prev; ++r) {  // (prev is the same for every thread)
+        Key best = 0;
+        for (int i = s0 + tid; i < s1; i += THREADS) {
           const float v = P::one(x + i);
-          if (v > bv && before(pv, pi, v, i)) {
-            bv = v;
-            bi = i;
-          }
+          const Key c = v > -f_inf() ? key_of(v, i) : 0;
+          if (c < prev && c > best) best = c;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-          const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-          const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-          if (oi >= 0 && (bi < 0 || before(ov, oi, bv, bi))) {
-            bv = ov;
-            bi = oi;
-          }
+          const Key c = __shfl_xor_sync(0xffffffffu, best, o);
+          best = c > best ? c : best;
         }
-        if (lane == 0) {
-          cv[warp] = bv;
-          ci[warp] = bi;
-        }
+        if (lane == 0) cand[warp] = best;
         __syncthreads();
-        bv = cv[0];
-        bi = ci[0];
-        for (int i = 1; i < WARPS; ++i)
-          if (ci[i] >= 0 && (bi < 0 || before(cv[i], ci[i], bv, bi))) {
-            bv = cv[i];
-            bi = ci[i];
-          }
+        best = cand[0];
+        for (int i = 1; i < WARPS; ++i) best = cand[i] > best ? cand[i] : best;
         __syncthreads();
-        pv = bv;
-        pi = bi;
-        if (tid == 0) {
-          tv[r] = bv;
-          ti[r] = bi;
-        }
-        if (bi < 0) break;  // (the same for every thread)
+        prev = best;
+        if (tid == 0) top[r] = best;
       }
     }
-  }
-  if (warp == 0) {
-    RowOut r = part[lane % WARPS];
-    join_lanes<WARPS>(r);
-    if (lane == 0) mine = r;
   }
   __syncthreads();
-  if (cl > 1) {
-    cluster_sync();
-    if (rank == 0) {
-      if (warp == 0) {
-        RowOut r{-f_inf(), 0.f, LOG2E, 0.f, 0.f, 0};
-        if (lane < cl) {
-          const uint32_t at = mapa_shared(smem_u32(&mine), lane);
-          r.m = __uint_as_float(ld_cluster(at));
-          r.r = __uint_as_float(ld_cluster(at + 4));
-          r.l = __uint_as_float(ld_cluster(at + 8));
-          r.s = __uint_as_float(ld_cluster(at + 12));
-          r.w = __uint_as_float(ld_cluster(at + 16));
-          r.bad = static_cast<int>(ld_cluster(at + 20));
-        }
-        join_lanes<MAX_CLUSTER>(r);
-        __syncwarp();
-        if (lane == 0) mine = r;
-      }
-      for (int c = tid; c < cl * k; c += THREADS) {  // at most 8 x 32 of CAP places
-        cv[c] = __uint_as_float(ld_cluster(mapa_shared(smem_u32(&tv[c % k]), c / k)));
-        ci[c] = static_cast<int>(ld_cluster(mapa_shared(smem_u32(&ti[c % k]), c / k)));
-      }
-      __syncthreads();
-      for (int c = tid; c < cl * k; c += THREADS) {
-        const float v = cv[c];
-        const int id = ci[c];
-        if (id < 0) continue;
-        int before_me = 0;
-        for (int i = 0; i < cl * k; ++i) before_me += ci[i] >= 0 && before(cv[i], ci[i], v, id);
-        if (before_me < k) {  // (rank 0's own list has been copied: its places are free)
-          tv[before_me] = v;
-          ti[before_me] = id;
-        }
-      }
-      __syncthreads();
+  if (cl > 1) {  // every block's results go to rank 0's shared memory
+    cluster_wait();
+    if (tid < k) st_cluster(mapa_shared(smem_u32(&all_top[rank * k + tid]), 0), top[tid]);
+    if (tid >= THREADS - static_cast<int>(sizeof(RowOut) / 4)) {
+      const int i = tid - (THREADS - static_cast<int>(sizeof(RowOut) / 4));
+      st_cluster(mapa_shared(smem_u32(&all[rank]) + 4 * i, 0), reinterpret_cast<const uint32_t*>(&mine)[i]);
     }
-    cluster_sync();  // the other blocks' shared memory is read: they may end
+    cluster_arrive();
+    cluster_wait();
     if (rank != 0) return;
+    if (warp == WARPS - 1) {
+      RowOut r{-f_inf(), 0.f, LOG2E, 0.f, 0.f, 0};
+      if (lane < cl) r = all[lane];
+      join_lanes<MAX_CLUSTER>(r);
+      __syncwarp();
+      if (lane == 0) mine = r;
+    }
+    const int n = cl * k;
+    if (tid < k) top[tid] = 0;
+    __syncthreads();
+    for (int c = tid; c < n; c += THREADS) {
+      const Key mk = all_top[c];
+      int before_me = 0;
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) before_me += all_top[i] > mk;
+      if (mk && before_me < k) top[before_me] = mk;
+    }
+    __syncthreads();
   }
   // a row with nothing left: with reference 0 and sum 1, x - m - log s is -infinity by itself
   const bool nan = mine.bad != 0, empty = !nan && !(mine.s > 0.f);
@@ -476,8 +453,8 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
     if (p.tokens) p.logprob[row] = nan || tok < -1 || tok >= p.V ? f_nan() : tok == -1 ? 0.f : (x_tok - m) - logs;
   }
   for (int r = tid; r < k; r += THREADS) {
-    p.top_id[row * k + r] = nan ? -1 : ti[r];
-    p.top_logprob[row * k + r] = nan ? f_nan() : (tv[r] - m) - logs;
+    p.top_id[row * k + r] = nan ? -1 : key_token(top[r]);
+    p.top_logprob[row * k + r] = nan ? f_nan() : (key_value(top[r]) - m) - logs;
   }
 }
 
