@@ -6,7 +6,6 @@ caller owns them); streams default to torch's current stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import os
 from typing import Dict, Optional, Sequence
@@ -448,33 +447,44 @@ def kva_op_gdn_scan(k: torch.Tensor, v: torch.Tensor, gb: torch.Tensor, state: t
                                 n_v, d, _stream(stream)), "kva_op_gdn_scan")
 
 
-def _one_device(stream, *tensors):
-    """The stream to launch on (given, or the current one of the tensors' device) and a context
-    in which that device is current.  Every tensor must be on that one CUDA device."""
-    dev = tensors[0].device
+def _one_device(stream, *tensors) -> tuple:
+    """(device index, stream to launch on): the stream given, or the current one of the tensors'
+    device.  Every tensor must be on that one CUDA device."""
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.device != dev or not t.is_cuda):
+        if t is not None and (t.get_device() != dev or dev < 0):
             raise ValueError("the tensors must be on one CUDA device")
-    here = dev.index == torch.cuda.current_device()
-    s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
-    return s, contextlib.nullcontext() if here else torch.cuda.device(dev)
+    return dev, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
 
 
-def _dense(t: Optional[torch.Tensor], shape, dtype, what: str) -> Optional[int]:
+def _call_on(dev: int, what: str, fn, *args) -> None:
+    """fn(*args) with device `dev` current, its status checked."""
+    if dev == torch.cuda.current_device():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status != KVA_OK:
+        raise KvaError(status, what)
+
+
+def _dense(t: Optional[torch.Tensor], shape: tuple, dtype, what: str) -> Optional[int]:
     """Pointer of a contiguous tensor of this shape and dtype (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, shape, what: str):
-    """(pointer, row stride) of a 2-D tensor of this shape whose rows are contiguous."""
-    if tuple(t.shape) != tuple(shape) or (shape[1] > 1 and t.stride(1) != 1):
+def _row_stride(t: torch.Tensor, shape, what: str) -> int:
+    """Row stride of a 2-D tensor of this shape whose rows are contiguous (over a single row it is
+    never used: the row's length)."""
+    rows, n = shape
+    if t.shape != shape or (n > 1 and t.stride(1) != 1):
         raise ValueError(f"{what} must be a row-major tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+    return t.stride(0) if rows > 1 else n
 
 
 def kva_op_gdn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gb: torch.Tensor,
@@ -485,34 +495,42 @@ def kva_op_gdn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gb: to
     include/kva_ops.h).  q, k [n_seq, T, n_k, d] and v, out [n_seq, T, n_v, d] in one 16-bit
     dtype, each token's heads contiguous (views into a wider row are fine); gb fp32
     [n_seq, 2, n_v, T] (g, then beta); state_in and state_out fp32 [n_seq, n_v, d, d] (the same
-    tensor: in place); lens: tokens of each sequence (host integers), default all T."""
-    n_seq, T, n_k, d = q.shape
-    n_v = v.shape[2]
-    s, on = _one_device(stream, q, k, v, gb, state_in, state_out, out, err)
-    a = KvaGdnForwardArgs(dtype=_DT[q.dtype], n_seq=n_seq, T=T, n_k=n_k, n_v=n_v, d=d, scale=scale)
-    for name, t, heads in (("q", q, n_k), ("k", k, n_k), ("v", v, n_v), ("out", out, n_v)):
-        if t.dtype != q.dtype or tuple(t.shape) != (n_seq, T, heads, d):
-            raise ValueError(f"{name} must be {q.dtype} {(n_seq, T, heads, d)}, got {t.dtype} {tuple(t.shape)}")
-        st = t.stride()
-        if st[3] != 1 or (heads > 1 and st[2] != d):
+    tensor: in place); lens: tokens of each sequence (host integers), default all T; err int32 [1]
+    receives device status bits."""
+    qk_shape, dt = q.shape, q.dtype
+    n_seq, T, n_k, d = qk_shape
+    v_shape = (n_seq, T, v.shape[2], d)
+    n_v = v_shape[2]
+    dev, s = _one_device(stream, q, k, v, gb, state_in, state_out, out, err)
+    strides = []
+    for name, t, shape in (("q", q, qk_shape), ("k", k, qk_shape), ("v", v, v_shape), ("out", out, v_shape)):
+        if t.dtype != dt or t.shape != shape:
+            raise ValueError(f"{name} must be {dt} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+        s_seq, s_tok, s_head, s_col = t.stride()
+        heads = shape[2]
+        if s_col != 1 or (heads > 1 and s_head != d):
             raise ValueError(f"the heads of a token of {name} must be contiguous")
-        setattr(a, name, t.data_ptr())
         # a stride over a single token or sequence is never used: one that passes the checks
-        ld = st[1] if T > 1 else heads * d
-        setattr(a, name + "_ld", ld)
-        setattr(a, name + "_seq", st[0] if n_seq > 1 else T * ld)
-    a.gb = _dense(gb, (n_seq, 2, n_v, T), torch.float32, "gb")
-    a.state_in = _dense(state_in, (n_seq, n_v, d, d), torch.float32, "state_in")
-    a.state_out = _dense(state_out, (n_seq, n_v, d, d), torch.float32, "state_out")
+        if T == 1:
+            s_tok = heads * d
+        strides.append(s_tok)
+        strides.append(s_seq if n_seq > 1 else T * s_tok)
+    S_shape = (n_seq, n_v, d, d)
+    c_lens = None
     if lens is not None:
         if len(lens) != n_seq:
             raise ValueError(f"lens must hold {n_seq} lengths, got {len(lens)}")
         if n_seq and not 0 <= min(lens) <= max(lens) <= T:
             raise ValueError(f"lens must lie in 0..{T}")
-        a.lens = (C.c_int32 * max(1, n_seq))(*lens)
-    with on:
-        _check(_lib.kva_op_gdn_forward(C.byref(a), _dense(err, (1,), torch.int32, "err"), s),
-               "kva_op_gdn_forward")
+        c_lens = (C.c_int32 * max(1, n_seq))(*lens)
+    a = KvaGdnForwardArgs(
+        _DT[dt], n_seq, T, n_k, n_v, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides[:6],
+        _dense(gb, (n_seq, 2, n_v, T), torch.float32, "gb"),
+        _dense(state_in, S_shape, torch.float32, "state_in"),
+        _dense(state_out, S_shape, torch.float32, "state_out"), out.data_ptr(), strides[6], strides[7],
+        c_lens, scale)
+    _call_on(dev, "kva_op_gdn_forward", _lib.kva_op_gdn_forward, C.byref(a),
+             _dense(err, (1,), torch.int32, "err"), s)
 
 
 def kva_op_add_rmsnorm(x: torch.Tensor, h: torch.Tensor, g: torch.Tensor, h_out: torch.Tensor,
@@ -521,25 +539,22 @@ def kva_op_add_rmsnorm(x: torch.Tensor, h: torch.Tensor, g: torch.Tensor, h_out:
     """h_out = h + x and out = RMSNorm(h_out) * g (see include/kva_ops.h): x, h, h_out, out
     [rows, n] with contiguous rows, g fp32 [n]; h_out may be h.  out bf16 / fp16, or int8 codes
     with fp16 scales [n / 32, rows] (q8_0, as kva_op_gemm_q8_0 reads it)."""
-    rows, n = x.shape
-    s, on = _one_device(stream, x, h, g, h_out, out, scales)
+    shape = x.shape
+    rows, n = shape
+    dev, s = _one_device(stream, x, h, g, h_out, out, scales)
     if h_out.dtype != h.dtype:
         raise ValueError("h and h_out must have one dtype")
-    px, ldx = _rows(x, (rows, n), "x")
-    ph, ldh = _rows(h, (rows, n), "h")
-    pho, ldho = _rows(h_out, (rows, n), "h_out")
-    po, ldo = _rows(out, (rows, n), "out")
-    if rows > 1 and ldh != ldho:
+    ldx, ldh = _row_stride(x, shape, "x"), _row_stride(h, shape, "h")
+    ldo = _row_stride(out, shape, "out")
+    if _row_stride(h_out, shape, "h_out") != ldh:
         raise ValueError("h and h_out must have one row stride")
     q8 = out.dtype == torch.int8
     if q8 != (scales is not None):
         raise ValueError("scales go with int8 codes, and with nothing else")
-    psc = _dense(scales, (n // 32, rows), torch.float16, "scales")
-    with on:
-        _check(_lib.kva_op_add_rmsnorm(px, _DT[x.dtype], ldx, ph, pho, _DT[h.dtype], ldh,
-                                       _dense(g, (n,), torch.float32, "g"), po,
-                                       KVA_Q8_0 if q8 else _DT[out.dtype], ldo, psc, rows, n, float(eps), s),
-               "kva_op_add_rmsnorm")
+    _call_on(dev, "kva_op_add_rmsnorm", _lib.kva_op_add_rmsnorm, x.data_ptr(), _DT[x.dtype], ldx,
+             h.data_ptr(), h_out.data_ptr(), _DT[h.dtype], ldh, _dense(g, (n,), torch.float32, "g"),
+             out.data_ptr(), KVA_Q8_0 if q8 else _DT[out.dtype], ldo,
+             _dense(scales, (n // 32, rows), torch.float16, "scales"), rows, n, eps, s)
 
 
 def kva_op_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None,
@@ -551,18 +566,16 @@ def kva_op_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] =
     int32 [rows], logprob / lse / entropy fp32 [rows], top_id int32 and top_logprob fp32
     [rows, n_top]."""
     rows, V = logits.shape
-    s, on = _one_device(stream, logits, tokens, logprob, lse, entropy, top_id, top_logprob)
-    px, ld = _rows(logits, (rows, V), "logits")
+    one, f32, i32 = (rows,), torch.float32, torch.int32
+    dev, s = _one_device(stream, logits, tokens, logprob, lse, entropy, top_id, top_logprob)
+    ld = _row_stride(logits, (rows, V), "logits")
     n_top = 0 if top_id is None else top_id.shape[-1]
     if (top_id is None) != (top_logprob is None) or (tokens is None) != (logprob is None):
         raise ValueError("top_id goes with top_logprob, tokens with logprob")
-    with on:
-        _check(_lib.kva_op_token_logprobs(
-            px, _DT[logits.dtype], ld, rows, V, _dense(tokens, (rows,), torch.int32, "tokens"),
-            _dense(logprob, (rows,), torch.float32, "logprob"), _dense(lse, (rows,), torch.float32, "lse"),
-            _dense(entropy, (rows,), torch.float32, "entropy"), n_top,
-            _dense(top_id, (rows, n_top), torch.int32, "top_id"),
-            _dense(top_logprob, (rows, n_top), torch.float32, "top_logprob"), s), "kva_op_token_logprobs")
+    _call_on(dev, "kva_op_token_logprobs", _lib.kva_op_token_logprobs, logits.data_ptr(), _DT[logits.dtype],
+             ld, rows, V, _dense(tokens, one, i32, "tokens"), _dense(logprob, one, f32, "logprob"),
+             _dense(lse, one, f32, "lse"), _dense(entropy, one, f32, "entropy"), n_top,
+             _dense(top_id, (rows, n_top), i32, "top_id"), _dense(top_logprob, (rows, n_top), f32, "top_logprob"), s)
 
 
 def kva_gdn_layer_update_noalloc(mixer_in: torch.Tensor, n_k: int, n_v: int, d: int,

@@ -99,8 +99,7 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(monkeypatch):
     with pytest.raises(ValueError, match="CUDA"):
         K.kva_op_token_logprobs(S[0, 0])
     # the binding's own shape checks, without a device: nothing may reach the library
-    import contextlib
-    monkeypatch.setattr(kmod, "_one_device", lambda *a: (0, contextlib.nullcontext()))
+    monkeypatch.setattr(kmod, "_one_device", lambda *a: (0, 0))
     for bad in (dict(lens=[4]), dict(lens=[-1]), dict(lens=[1, 1]), dict(lens=[2 ** 32]), dict(gb=gb[:, :1]),
                 dict(state_in=S.half()), dict(state_out=S.transpose(2, 3)), dict(v=v.bfloat16()),
                 dict(k=q[..., ::2]), dict(k=q.transpose(1, 2)), dict(out=v[:, :2])):
