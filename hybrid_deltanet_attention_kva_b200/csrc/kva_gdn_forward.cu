@@ -585,8 +585,8 @@ struct Tc {
   static constexpr int SC = XH + 2 * XM;              // fp32 [64]: e^gam, beta e^gam, beta, e^(gam_last-gam); e^gam_last
   static constexpr int SC_BYTES = (4 * TC_C + 8) * 4; // two stages
   static constexpr int LD = SC + 2 * SC_BYTES;        // L's diagonal blocks, fp32
-  static constexpr int GAM = LD + 4 * 16 * 64;        // gam as two floats, beta: [3][64], two chunks'
-  static constexpr int BAR = GAM + 2 * 3 * TC_C * 4;      // full[2], used[2], y, u, s, o, drain
+  static constexpr int GAM = LD + 4 * 16 * 64;        // gam as two floats, beta: [3][64]
+  static constexpr int BAR = GAM + 3 * TC_C * 4;      // full[2], used[2], y, u, s, o, drain
   static constexpr int MISC = BAR + 9 * 8;            // TMEM base, abort flag
   static constexpr int BYTES = MISC + 16;
   static constexpr int ALLOC = BYTES + 1024;          // slack for 1024-byte alignment
@@ -607,9 +607,9 @@ __device__ __forceinline__ void store_pair(uint8_t* hi_at, uint8_t* lo_at, uint3
 }
 
 // X's blocks below the diagonal in columns [16 JB + 8 hf, + 8): X_ij = -X_ii sum_{k=j}^{i-1} L_ik X_kj.
-// XH and XL are [64][64] tiles, X's two terms; L_ik waits in the place of their (zero) block (k, i).
+// L's blocks lie as two terms in lh / ll, X's in xh / xl (shared addresses of [64][64] tiles).
 template <typename T, int JB>
-__device__ __forceinline__ void off_diagonal(uint8_t* XH, uint8_t* XL, int hf, int lane) {
+__device__ __forceinline__ void off_diagonal(uint8_t* XH, uint8_t* XL, uint32_t lh, uint32_t ll, int hf, int lane) {
   const int mi = lane >> 3, lr = lane & 7, gr = lane >> 2, cq = lane & 3;
   const uint32_t xh = smem_u32(XH), xl = smem_u32(XL);
   const int s0 = 16 * JB + 8 * hf;
@@ -622,9 +622,9 @@ __device__ __forceinline__ void off_diagonal(uint8_t* XH, uint8_t* XL, int hf, i
     uint32_t ah[4], al[4];
 #pragma unroll
     for (int k = JB; k < i; ++k) {
-      const uint32_t o = piece<128>(16 * k + (mi & 1) * 8 + lr, 2 * i + (mi >> 1));
-      ldmatrix_x4(ah, xh + o);
-      ldmatrix_x4(al, xl + o);
+      const uint32_t o = piece<128>(16 * i + (mi & 1) * 8 + lr, 2 * k + (mi >> 1));
+      ldmatrix_x4(ah, lh + o);
+      ldmatrix_x4(al, ll + o);
       mma_tile(T(), y, al, bh[k][0], bh[k][1]);
       mma_tile(T(), y, ah, bl[k][0], bl[k][1]);
       mma_tile(T(), y, ah, bh[k][0], bh[k][1]);
@@ -656,7 +656,7 @@ __device__ __forceinline__ void off_diagonal(uint8_t* XH, uint8_t* XL, int hf, i
   }
 }
 
-// The preparing warps.
+// The preparing warps: warp w owns tokens [16 w, 16 w + 16) of K K^T, Q K^T, L and M.
 template <typename T>
 __device__ void tc_prepare(const GdnFwd& p, uint8_t* sm, int h, int seq, int len, int tid, volatile int* abort_flag) {
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + Tc::BAR);
@@ -680,7 +680,7 @@ __device__ void tc_prepare(const GdnFwd& p, uint8_t* sm, int h, int seq, int len
     const T* kp = k + t0 * p.k_ld + 8 * xc;
     const T* qp = q + t0 * p.q_ld + 8 * xc;
     const T* vp = v + t0 * p.v_ld + 8 * xc;
-#pragma unroll 2
+#pragma unroll
     for (int i = 0; i < TC_C / 8; ++i) {
       const bool on = t0 + 8 * i < len;
       const uint32_t o = piece<128>(8 * i + r0, xc & 7);
@@ -692,138 +692,125 @@ __device__ void tc_prepare(const GdnFwd& p, uint8_t* sm, int h, int seq, int len
       vp += 8 * p.v_ld;
     }
   };
-  // warp 3: a chunk's gates, tokens 2 lane and 2 lane + 1 (zero past the end: steps that do nothing)
-  float ga = 0.f, gb = 0.f, ba = 0.f, bb = 0.f;  // the next chunk's, loaded ahead
+  // warp 0: gates of tokens 2 lane and 2 lane + 1
+  float g0n = 0.f, g1n = 0.f, b0n = 0.f, b1n = 0.f;
   auto load_gates = [&](int c) {
     const int64_t t = static_cast<int64_t>(c) * TC_C + 2 * lane;
-    ga = t < len ? g[t] : 0.f;
-    ba = t < len ? b[t] : 0.f;
-    gb = t + 1 < len ? g[t + 1] : 0.f;
-    bb = t + 1 < len ? b[t + 1] : 0.f;
-  };
-  float s0, s0l, s1, s1l, sb0, sb1;  // cumulative decays and betas of those tokens
-  auto sum_gates = [&](int c) {
-    // e^g is 0 in fp32 from -104 on; the clamp keeps -infinity out of the differences
-    const float x = ga < -1000.f ? -1000.f : ga, y = gb < -1000.f ? -1000.f : gb;
-    sb0 = ba;
-    sb1 = bb;
-    // cumulative decays as unevaluated sums of two floats (see above)
-    float s = x + y, r = s - x, sl = (x - (s - r)) + (y - r);
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      const float z = __shfl_up_sync(0xffffffffu, s, o), zl = __shfl_up_sync(0xffffffffu, sl, o);
-      if (lane >= o) {
-        const float n = s + z;
-        r = n - s;
-        sl += zl + ((s - (n - r)) + (z - r));
-        s = n;
-      }
-    }
-    s1 = s;
-    s1l = sl;
-    s0 = s - y;  // the pair's sum without its second gate
-    r = s0 - s;
-    s0l = sl + ((s - (s0 - r)) + (-y - r));
-    float2* f = reinterpret_cast<float2*>(sm + Tc::GAM + (c & 1) * 3 * TC_C * 4);
-    f[lane] = make_float2(s0, s1);
-    f[32 + lane] = make_float2(s0l, s1l);
-    f[64 + lane] = make_float2(sb0, sb1);
-    load_gates(c + 1);  // (past the last chunk: zeros)
-  };
-  auto store_scalars = [&](int c) {
-    const float last = __shfl_sync(0xffffffffu, s1, 31), lastl = __shfl_sync(0xffffffffu, s1l, 31);
-    float2* f = reinterpret_cast<float2*>(sm + Tc::SC + (c & 1) * Tc::SC_BYTES);
-    const float e0 = expf(s0 + s0l), e1 = expf(s1 + s1l);
-    f[lane] = make_float2(e0, e1);
-    f[32 + lane] = make_float2(sb0 * e0, sb1 * e1);
-    f[64 + lane] = make_float2(sb0, sb1);
-    f[96 + lane] = make_float2(expf((last - s0) + (lastl - s0l)), expf((last - s1) + (lastl - s1l)));
-    if (lane == 0) f[128] = make_float2(expf(last + lastl), 0.f);
+    g0n = t < len ? g[t] : 0.f;
+    b0n = t < len ? b[t] : 0.f;
+    g1n = t + 1 < len ? g[t + 1] : 0.f;
+    b1n = t + 1 < len ? b[t + 1] : 0.f;
   };
   if (n_chunks > 0) load(0);
   cp_async_commit();
   if (n_chunks > 1) load(1);
   cp_async_commit();
-  if (w == 3) {
-    load_gates(0);
-    sum_gates(0);
-    store_scalars(0);
-  }
+  if (w == 0) load_gates(0);
   // the blocks above X's and M's diagonals stay zero
   for (int i = tid; i < 2 * Tc::XM / 16; i += TC_PREP)
     reinterpret_cast<uint4*>(sm + Tc::XH)[i] = make_uint4(0u, 0u, 0u, 0u);
 
+  float* gh = reinterpret_cast<float*>(sm + Tc::GAM);
+  float* glo = gh + TC_C;
+  float* bet = gh + 2 * TC_C;
   for (int c = 0; c < n_chunks; ++c) {
     uint8_t* XH = sm + Tc::XH + (c & 1) * Tc::XM;
     uint8_t* XL = XH + Tc::TILE;
     uint8_t* MH = XL + Tc::TILE;
     uint8_t* ML = MH + Tc::TILE;
     const uint32_t st = base + (c % 3) * Tc::IN;
-    const float* gh = reinterpret_cast<const float*>(sm + Tc::GAM) + (c & 1) * 3 * TC_C;
-    const float *glo = gh + TC_C, *bet = gh + 2 * TC_C;
-    cp_async_wait<1>();
-    bar_sync(2, TC_PREP);  // the chunk's rows, gam and beta are there for every preparing warp
-    // the ten blocks (i, j), j <= i, of K K^T and Q K^T, of L and M, dealt to the warps.  e^(gam_t - gam_s):
-    // directly in a diagonal block, below it as a product around the last token of block row i - 1; the
-    // fast exponential is off by 2^-22 + |x| 2^-24, and what is far has no weight.  (Rolled: the two
-    // roles' code together has to stay in the instruction cache.)
-#pragma unroll 1
-    for (int blk = w; blk < 10; blk += 4) {
-      const int i = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, j = blk - i * (i + 1) / 2;
-      float kk[2][4] = {}, qk[2][4] = {};
-      // (piece (2 k + m) ^ r of a row is (m ^ r) ^ 2 k: one exclusive or a step)
-      const uint32_t at = st + piece<128>((mi & 1) * 8 + lr, mi >> 1);
-#pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        const uint32_t ka = at + hf * Tc::HALF + 16 * 128 * i, qa = ka + Tc::Q, kb = at + hf * Tc::HALF + 16 * 128 * j;
-        uint32_t a[4][4], x[4][4], y[4][4];
+    if (w == 0) {
+      float ga = g0n, gb = g1n;
+      const float ba = b0n, bb = b1n;
+      load_gates(c + 1);  // (past the last chunk: zeros)
+      // e^g is 0 in fp32 from -104 on; the clamp keeps -infinity out of the differences
+      ga = ga < -1000.f ? -1000.f : ga;
+      gb = gb < -1000.f ? -1000.f : gb;
+      // cumulative decays as unevaluated sums of two floats (see above)
+      float s = ga + gb, r = s - ga, sl = (ga - (s - r)) + (gb - r);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          ldmatrix_x4(a[ks], ka ^ (ks << 5));
-          ldmatrix_x4(y[ks], kb ^ (ks << 5));
-          ldmatrix_x4(x[ks], qa ^ (ks << 5));
-        }
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          mma_n<T>(kk[0], kk[1], a[ks], y[ks]);
-          mma_n<T>(qk[0], qk[1], x[ks], y[ks]);
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, s, o), yl = __shfl_up_sync(0xffffffffu, sl, o);
+        if (lane >= o) {
+          const float z = s + y;
+          r = z - s;
+          sl += yl + ((s - (z - r)) + (y - r));
+          s = z;
         }
       }
-      const int t0 = 16 * i + gr, t1 = t0 + 8;
+      // token 2 lane: the pair's sum without its second gate
+      const float s1 = s - gb;
+      r = s1 - s;
+      const float s1l = sl + ((s - (s1 - r)) + (-gb - r));
+      const float last = __shfl_sync(0xffffffffu, s, 31), lastl = __shfl_sync(0xffffffffu, sl, 31);
+      reinterpret_cast<float2*>(gh)[lane] = make_float2(s1, s);
+      reinterpret_cast<float2*>(glo)[lane] = make_float2(s1l, sl);
+      reinterpret_cast<float2*>(bet)[lane] = make_float2(ba, bb);
+      float2* f = reinterpret_cast<float2*>(sm + Tc::SC + (c & 1) * Tc::SC_BYTES);
+      const float e0 = expf(s1 + s1l), e1 = expf(s + sl);
+      f[lane] = make_float2(e0, e1);
+      f[32 + lane] = make_float2(ba * e0, bb * e1);
+      f[64 + lane] = make_float2(ba, bb);
+      f[96 + lane] = make_float2(expf((last - s1) + (lastl - s1l)), expf((last - s) + (lastl - sl)));
+      if (lane == 0) f[128] = make_float2(expf(last + lastl), 0.f);
+    }
+    cp_async_wait<1>();
+    bar_sync(2, TC_PREP);  // the chunk's rows, gam and beta are there for every preparing warp
+    float kk[4][2][4] = {}, qk[4][2][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < TC_D / 16; ++ks) {
+      const uint32_t half = st + (ks >> 2) * Tc::HALF;
+      const int pc = 2 * (ks & 3) + (mi >> 1), pr = (mi & 1) * 8 + lr;
+      uint32_t a[4], x[4], y[4];
+      ldmatrix_x4(a, half + Tc::K + piece<128>(16 * w + pr, pc));
+      ldmatrix_x4(x, half + Tc::Q + piece<128>(16 * w + pr, pc));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j > w) continue;  // (the same for the whole warp)
+        ldmatrix_x4(y, half + Tc::K + piece<128>(16 * j + pr, pc));
+        mma_n<T>(kk[j][0], kk[j][1], a, y);
+        mma_n<T>(qk[j][0], qk[j][1], x, y);
+      }
+    }
+    // L and M: e^(gam_t - gam_s) directly in the diagonal block, below it as a product around the last
+    // token of the block row before.  L's blocks below the diagonal wait in M's place
+    {
+      const int t0 = 16 * w + gr, t1 = t0 + 8;
       const float h0 = gh[t0], h1 = gh[t1], l0 = glo[t0], l1 = glo[t1], b0 = bet[t0], b1 = bet[t1];
-      const float rh = i ? gh[16 * i - 1] : 0.f, rl = i ? glo[16 * i - 1] : 0.f;
+      const float rh = w ? gh[16 * w - 1] : 0.f, rl = w ? glo[16 * w - 1] : 0.f;
       const float rf0 = __expf((h0 - rh) + (l0 - rl)), rf1 = __expf((h1 - rh) + (l1 - rl));
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int s = 16 * j + 8 * e + 2 * cq, sc = s & 15;
-        const float2 gs = *reinterpret_cast<const float2*>(gh + s), ls = *reinterpret_cast<const float2*>(glo + s);
-        float d[4];
-        if (j < i) {
-          const float c0 = __expf((rh - gs.x) + (rl - ls.x)), c1 = __expf((rh - gs.y) + (rl - ls.y));
-          d[0] = rf0 * c0;
-          d[1] = rf0 * c1;
-          d[2] = rf1 * c0;
-          d[3] = rf1 * c1;
-          const uint32_t o0 = piece<128>(16 * j + gr, 2 * i + e) + 4 * cq, o1 = piece<128>(16 * j + gr + 8, 2 * i + e) + 4 * cq;
-          store_pair<T>(XH, XL, o0, b0 * d[0] * kk[e][0], b0 * d[1] * kk[e][1]);
-          store_pair<T>(XH, XL, o1, b1 * d[2] * kk[e][2], b1 * d[3] * kk[e][3]);
-        } else {  // (chosen, not multiplied by 0, above the diagonal: the decay there may be infinite)
-          d[0] = s <= t0 ? __expf((h0 - gs.x) + (l0 - ls.x)) : 0.f;
-          d[1] = s + 1 <= t0 ? __expf((h0 - gs.y) + (l0 - ls.y)) : 0.f;
-          d[2] = s <= t1 ? __expf((h1 - gs.x) + (l1 - ls.x)) : 0.f;
-          d[3] = s + 1 <= t1 ? __expf((h1 - gs.y) + (l1 - ls.y)) : 0.f;
-          uint8_t* ld = sm + Tc::LD + i * 16 * 64;
-          *reinterpret_cast<float2*>(ld + piece_f(gr, sc >> 2) + (sc & 3) * 4) =
-              make_float2(s < t0 ? b0 * d[0] * kk[e][0] : 0.f, s + 1 < t0 ? b0 * d[1] * kk[e][1] : 0.f);
-          *reinterpret_cast<float2*>(ld + piece_f(gr + 8, sc >> 2) + (sc & 3) * 4) =
-              make_float2(s < t1 ? b1 * d[2] * kk[e][2] : 0.f, s + 1 < t1 ? b1 * d[3] * kk[e][3] : 0.f);
-          if (s > t0) qk[e][0] = 0.f;
-          if (s + 1 > t0) qk[e][1] = 0.f;
-          if (s > t1) qk[e][2] = 0.f;
-          if (s + 1 > t1) qk[e][3] = 0.f;
+      for (int j = 0; j < 4; ++j) {
+        if (j > w) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int s = 16 * j + 8 * i + 2 * cq;
+          const float2 gs = *reinterpret_cast<const float2*>(gh + s), ls = *reinterpret_cast<const float2*>(glo + s);
+          float(&x)[4] = kk[j][i];
+          float(&m)[4] = qk[j][i];
+          if (j < w) {
+            const float c0 = __expf((rh - gs.x) + (rl - ls.x)), c1 = __expf((rh - gs.y) + (rl - ls.y));
+            m[0] *= rf0 * c0;
+            m[1] *= rf0 * c1;
+            m[2] *= rf1 * c0;
+            m[3] *= rf1 * c1;
+            store_pair<T>(MH, ML, piece<128>(t0, s >> 3) + 4 * cq, b0 * rf0 * c0 * x[0], b0 * rf0 * c1 * x[1]);
+            store_pair<T>(MH, ML, piece<128>(t1, s >> 3) + 4 * cq, b1 * rf1 * c0 * x[2], b1 * rf1 * c1 * x[3]);
+          } else {
+            const float d0 = __expf((h0 - gs.x) + (l0 - ls.x)), d1 = __expf((h0 - gs.y) + (l0 - ls.y));
+            const float d2 = __expf((h1 - gs.x) + (l1 - ls.x)), d3 = __expf((h1 - gs.y) + (l1 - ls.y));
+            uint8_t* ld = sm + Tc::LD + w * 16 * 64;
+            const int sc = s & 15;
+            *reinterpret_cast<float2*>(ld + piece_f(gr, sc >> 2) + (sc & 3) * 4) =
+                make_float2(s < t0 ? b0 * d0 * x[0] : 0.f, s + 1 < t0 ? b0 * d1 * x[1] : 0.f);
+            *reinterpret_cast<float2*>(ld + piece_f(gr + 8, sc >> 2) + (sc & 3) * 4) =
+                make_float2(s < t1 ? b1 * d2 * x[2] : 0.f, s + 1 < t1 ? b1 * d3 * x[3] : 0.f);
+            m[0] = s <= t0 ? d0 * m[0] : 0.f;
+            m[1] = s + 1 <= t0 ? d1 * m[1] : 0.f;
+            m[2] = s <= t1 ? d2 * m[2] : 0.f;
+            m[3] = s + 1 <= t1 ? d3 * m[3] : 0.f;
+          }
         }
-        store_pair<T>(MH, ML, piece<128>(t0, 2 * j + e) + 4 * cq, d[0] * qk[e][0], d[1] * qk[e][1]);
-        store_pair<T>(MH, ML, piece<128>(t1, 2 * j + e) + 4 * cq, d[2] * qk[e][2], d[3] * qk[e][3]);
       }
     }
     bar_sync(2, TC_PREP);
@@ -858,22 +845,25 @@ __device__ void tc_prepare(const GdnFwd& p, uint8_t* sm, int h, int seq, int len
         *reinterpret_cast<uint4*>(XH + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(XL + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
-    } else if (w == 3) {
-      sum_gates(c + 1);
     }
     bar_sync(2, TC_PREP);
+    const uint32_t lh = smem_u32(MH), ll = smem_u32(ML);
     if (w < 2) {
-      off_diagonal<T, 0>(XH, XL, w, lane);
+      off_diagonal<T, 0>(XH, XL, lh, ll, w, lane);
     } else {
-      off_diagonal<T, 1>(XH, XL, w - 2, lane);
-      off_diagonal<T, 2>(XH, XL, w - 2, lane);
+      off_diagonal<T, 1>(XH, XL, lh, ll, w - 2, lane);
+      off_diagonal<T, 2>(XH, XL, lh, ll, w - 2, lane);
     }
-    bar_sync(2, TC_PREP);  // L is read: its place is zero again
-    for (int i = tid; i < 6 * 32; i += TC_PREP) {
-      const int blk = i >> 5, k = blk < 3 ? 0 : blk < 5 ? 1 : 2, j = blk < 3 ? blk + 1 : blk < 5 ? blk - 1 : 3;
-      const uint32_t o = piece<128>(16 * k + (i >> 1 & 15), 2 * j + (i & 1));
-      *reinterpret_cast<uint4*>(XH + o) = make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(XL + o) = make_uint4(0u, 0u, 0u, 0u);
+    bar_sync(2, TC_PREP);  // L is read: M takes its place
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j > w) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int pc = 2 * j + i;
+        store_pair<T>(MH, ML, piece<128>(16 * w + gr, pc) + 4 * cq, qk[j][i][0], qk[j][i][1]);
+        store_pair<T>(MH, ML, piece<128>(16 * w + gr + 8, pc) + 4 * cq, qk[j][i][2], qk[j][i][3]);
+      }
     }
     fence_proxy_async_smem();  // rows, X and M are read by the tensor cores
     bar_sync(2, TC_PREP);
@@ -886,29 +876,8 @@ __device__ void tc_prepare(const GdnFwd& p, uint8_t* sm, int h, int seq, int len
     }
     if (c + 2 < n_chunks) load(c + 2);
     cp_async_commit();
-    if (w == 3 && c + 1 < n_chunks) store_scalars(c + 1);
   }
   cp_async_wait<0>();
-}
-
-// MMAs (A in tensor memory) and commits for a converged warp of which one lane, `on`, issues: with the
-// predicate on the instruction alone, its operands stay in the warp's uniform registers.
-__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(on)
-      : "memory");
-}
-__device__ __forceinline__ void commit_on(uint32_t on, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-      "r"(on)
-      : "memory");
 }
 
 // A wait of the main warps; on giving up, the flag ends every other wait of the block too.
@@ -929,7 +898,7 @@ __device__ void tc_main(const GdnFwd& p, uint8_t* sm, int h, int seq, int len, i
   const int row = 32 * qd + lane, n_chunks = (len + TC_C - 1) / TC_C;
   const uint32_t tl = tb + (static_cast<uint32_t>(32 * qd) << 16);
   const int64_t srow = ((static_cast<int64_t>(seq) * p.n_v + h) * TC_D + row) * TC_D + 64 * hc;
-  T* out = static_cast<T*>(p.out) + seq * p.out_seq + h * TC_D + 32 * qd + (lane & 24);
+  T* out = static_cast<T*>(p.out) + seq * p.out_seq + h * TC_D + row;
   constexpr uint32_t FMT = F16<T>::umma_fmt;
   constexpr uint32_t ID_128 = idesc_f16kind_f32_major(128, 128, FMT, false, false);
   constexpr uint32_t ID_64 = idesc_f16kind_f32_major(128, 64, FMT, false, false);
@@ -960,41 +929,11 @@ __device__ void tc_main(const GdnFwd& p, uint8_t* sm, int h, int seq, int len, i
     uint32_t r[32];
     tmem_ld_32x32b_x32(tl + TM_O + 32 * hc, r);
     tmem_ld_wait();
-    // a lane has 32 tokens of one column: eight lanes trade 8 x 8 blocks, so that each stores 16 bytes of
-    // four tokens (32 two-byte stores a lane kept the load/store unit busy for 3400 cycles)
-    const int64_t t0 = static_cast<int64_t>(c) * TC_C + 32 * hc + (lane & 7);
+    const int64_t t0 = static_cast<int64_t>(c) * TC_C + 32 * hc;
     T* o = out + t0 * p.out_ld;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t x[4];  // tokens 8 e + 2 i, + 1 of this lane's column
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        x[i] = F16<T>::pack(p.scale * (zr[8 * e + 2 * i] + u2f(r[8 * e + 2 * i])),
-                            p.scale * (zr[8 * e + 2 * i + 1] + u2f(r[8 * e + 2 * i + 1])));
-      // token bit 0 against column bit 0, then bits 1 and 2
-      const bool o1 = lane & 1, o2 = lane & 2, o4 = lane & 4;
-      uint32_t y[4], z[4];
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const uint32_t s = __shfl_xor_sync(0xffffffffu, __byte_perm(x[i], x[i + 1], o1 ? 0x5410 : 0x7632), 1);
-        y[i] = o1 ? __byte_perm(x[i], s, 0x3254) : __byte_perm(x[i], s, 0x5410);
-        y[i + 1] = o1 ? __byte_perm(x[i + 1], s, 0x3276) : __byte_perm(x[i + 1], s, 0x7610);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const uint32_t s = __shfl_xor_sync(0xffffffffu, o2 ? y[i] : y[i + 1], 2);
-        z[i] = o2 ? s : y[i];
-        z[i + 1] = o2 ? y[i + 1] : s;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t s = __shfl_xor_sync(0xffffffffu, o4 ? z[i] : z[i + 2], 4);
-        y[i] = o4 ? s : z[i];
-        y[i + 2] = o4 ? z[i + 2] : s;
-      }
-      if (t0 + 8 * e < len) *reinterpret_cast<uint4*>(o) = make_uint4(y[0], y[1], y[2], y[3]);
-      o += 8 * p.out_ld;
-    }
+    for (int j = 0; j < 32; ++j)
+      if (t0 + j < len) o[j * p.out_ld] = F16<T>::from(p.scale * (zr[j] + u2f(r[j])));
   };
 
   for (int c = 0; c < n_chunks; ++c) {
@@ -1007,7 +946,7 @@ __device__ void tc_main(const GdnFwd& p, uint8_t* sm, int h, int seq, int len, i
     // pass 1
     {
       const float gl = sc[4 * TC_C];
-#pragma unroll 1
+#pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t r[32], hi[16], lo[16];
         tmem_ld_32x32b_x32(tl + TM_S + 64 * hc + 32 * i, r);
@@ -1028,16 +967,15 @@ __device__ void tc_main(const GdnFwd& p, uint8_t* sm, int h, int seq, int len, i
     bar_sync(1, TC_MAIN);
     if (warp == 0) {
       tc_fence_after();
-      const uint32_t on = __any_sync(0xffffffffu, *abort_flag) ? 0u : issuer;
-      {
+      if (issuer && !*abort_flag) {
         const uint64_t d = sdesc_k_sw128(kq);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          mma_ts(on, tb + TM_Y, tb + TM_A + 8 * j, d + (((j >> 2) * Tc::HALF + (j & 3) * 32) >> 4), ID_128, j > 0);
+          umma_f16_ts(tb + TM_Y, tb + TM_A + 8 * j, d + (((j >> 2) * Tc::HALF + (j & 3) * 32) >> 4), ID_128, j > 0);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          mma_ts(on, tb + TM_Y, tb + TM_A + 64 + 8 * j, d + (((j >> 2) * Tc::HALF + (j & 3) * 32) >> 4), ID_64, 1);
-        commit_on(on, ybar);
+          umma_f16_ts(tb + TM_Y, tb + TM_A + 64 + 8 * j, d + (((j >> 2) * Tc::HALF + (j & 3) * 32) >> 4), ID_64, 1);
+        umma_commit(ybar);
       }
       __syncwarp();
     }
@@ -1068,16 +1006,15 @@ __device__ void tc_main(const GdnFwd& p, uint8_t* sm, int h, int seq, int len, i
     bar_sync(1, TC_MAIN);
     if (warp == 0) {
       tc_fence_after();
-      const uint32_t on = __any_sync(0xffffffffu, *abort_flag) ? 0u : issuer;
-      {
+      if (issuer && !*abort_flag) {
         const uint64_t dh = sdesc_k_sw128(xh), dl = sdesc_k_sw128(xh + Tc::TILE);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_ts(on, tb + TM_U, tb + TM_A + 32 + 8 * j, dh + 2 * j, ID_64, j > 0);
+        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_U, tb + TM_A + 32 + 8 * j, dh + 2 * j, ID_64, j > 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_ts(on, tb + TM_U, tb + TM_A + 8 * j, dl + 2 * j, ID_64, 1);
+        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_U, tb + TM_A + 8 * j, dl + 2 * j, ID_64, 1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_ts(on, tb + TM_U, tb + TM_A + 8 * j, dh + 2 * j, ID_64, 1);
-        commit_on(on, ubar);
+        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_U, tb + TM_A + 8 * j, dh + 2 * j, ID_64, 1);
+        umma_commit(ubar);
       }
       __syncwarp();
     }
@@ -1114,23 +1051,22 @@ __device__ void tc_main(const GdnFwd& p, uint8_t* sm, int h, int seq, int len, i
     bar_sync(1, TC_MAIN);
     if (warp == 0) {
       tc_fence_after();
-      const uint32_t on = __any_sync(0xffffffffu, *abort_flag) ? 0u : issuer;
-      {
+      if (issuer && !*abort_flag) {
         const uint64_t dk = sdesc_mn_sw128(kq, Tc::HALF);
         const uint64_t mh = sdesc_k_sw128(xh + 2 * Tc::TILE), ml = sdesc_k_sw128(xh + 3 * Tc::TILE);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_ts(on, tb + TM_S, tb + TM_A + 32 + 8 * j, dk + ((j * 2048) >> 4), ID_S, 1);
+        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_S, tb + TM_A + 32 + 8 * j, dk + ((j * 2048) >> 4), ID_S, 1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_ts(on, tb + TM_S, tb + TM_A + 8 * j, dk + ((j * 2048) >> 4), ID_S, 1);
-        commit_on(on, sbar);
+        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_S, tb + TM_A + 8 * j, dk + ((j * 2048) >> 4), ID_S, 1);
+        umma_commit(sbar);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_ts(on, tb + TM_O, tb + TM_Y + 32 + 8 * j, mh + 2 * j, ID_64, j > 0);
+        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_O, tb + TM_Y + 32 + 8 * j, mh + 2 * j, ID_64, j > 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_ts(on, tb + TM_O, tb + TM_Y + 8 * j, ml + 2 * j, ID_64, 1);
+        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_O, tb + TM_Y + 8 * j, ml + 2 * j, ID_64, 1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_ts(on, tb + TM_O, tb + TM_Y + 8 * j, mh + 2 * j, ID_64, 1);
-        commit_on(on, obar);
-        commit_on(on, &used[c & 1]);
+        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_O, tb + TM_Y + 8 * j, mh + 2 * j, ID_64, 1);
+        umma_commit(obar);
+        umma_commit(&used[c & 1]);
       }
       __syncwarp();
     }
