@@ -27,8 +27,6 @@ struct GdnFwd {
 
 // runs of at most this many tokens go token by token
 constexpr int kStepTokens = 8;
-// 128-dim heads: sequences from this many tokens on go to the tensor-memory kernel
-constexpr int kTcTokens = 48;
 
 // 4 consecutive 16-bit values as floats
 template <typename T>
@@ -163,11 +161,6 @@ __device__ __forceinline__ uint32_t piece16(int r, int c) {
   return static_cast<uint32_t>(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
 }
 
-// and in a [16][16] fp32 block (64-byte rows)
-__device__ __forceinline__ uint32_t piece_f(int r, int c) {
-  return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-}
-
 // x as two 16-bit terms: hi + lo holds x to the square of the type's half step
 template <typename T>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -194,12 +187,6 @@ __device__ __forceinline__ void mma_tile(__nv_bfloat16, float (&d)[4], const uin
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// two neighbouring column tiles with a B fragment of ldmatrix.x4 whose rows are B's columns
-template <typename T>
-__device__ __forceinline__ void mma_n(float (&d0)[4], float (&d1)[4], const uint32_t (&a)[4], const uint32_t (&b)[4]) {
-  mma_tile(T(), d0, a, b[0], b[2]);
-  mma_tile(T(), d1, a, b[1], b[3]);
 }
 template <typename T>
 __device__ __forceinline__ void mma2(float (&d0)[4], float (&d1)[4], const uint32_t (&a)[4], const uint32_t (&b)[4],
@@ -557,587 +544,10 @@ __global__ void __launch_bounds__(kChunkThreads, 2) gdn_chunk_kernel(const __gri
   else prepare_runs<T, D>(p, sm, h, half, seq, len, warp - CHAIN, lane, abort_flag);
 }
 
-// ============================================================================
-// 128-dim heads, chunks of 64 tokens on the fifth-generation tensor cores: the same formulas as
-// above with a block per head.  The state (128 x 128 fp32) lives in tensor memory, lane v holding
-// row v.  Eight main warps (two per lane quarter, each with half of the columns) convert between the
-// products, one elected lane of warp 0 issues them, four preparing warps work a chunk ahead:
-//     pass 1: A <- S in two 16-bit terms,  S <- e^gam_last S
-//     MMA   : [Y | Z] = S [K ; Q]^T           | the readout of the chunk before is written meanwhile
-//     pass 2: A <- W in two terms (rows of V from shared memory)
-//     MMA   : U = W X^T                       | Z diag(e^gam) to registers meanwhile
-//     pass 3: A <- U diag(e^(gam_last-gam)), B <- U, in two terms each
-//     MMA   : S += U diag(..) K, then O = U M^T
-// Two terms an operand cost two (with a 16-bit partner) or three MMAs and keep the fp32 state
-// free of 16-bit roundings.
-// ============================================================================
-constexpr int TC_MAIN = 256, TC_PREP = 128, TC_D = 128, TC_C = 64;
-constexpr uint32_t TM_S = 0, TM_A = 128, TM_Y = 256, TM_Z = 320, TM_U = 384, TM_O = 448, TM_COLS = 512;
-
-struct Tc {
-  static constexpr int TILE = TC_C * TC_C * 2;        // [64][64] 16-bit, 128-byte rows, pieces xor-swizzled
-  static constexpr int K = 0, Q = TILE;               // columns 0-63; columns 64-127 HALF further
-  static constexpr int HALF = 2 * TILE;
-  static constexpr int V = 2 * HALF;                  // two [64][64] halves
-  static constexpr int IN = V + 2 * TILE;             // bytes of a chunk's inputs, three stages
-  static constexpr int XH = 3 * IN;                   // X, then M, two terms each; two stages
-  static constexpr int XM = 4 * TILE;
-  static constexpr int SC = XH + 2 * XM;              // fp32 [64]: e^gam, beta e^gam, beta, e^(gam_last-gam); e^gam_last
-  static constexpr int SC_BYTES = (4 * TC_C + 8) * 4; // two stages
-  static constexpr int LD = SC + 2 * SC_BYTES;        // L's diagonal blocks, fp32
-  static constexpr int GAM = LD + 4 * 16 * 64;        // gam as two floats, beta: [3][64]
-  static constexpr int BAR = GAM + 3 * TC_C * 4;      // full[2], used[2], y, u, s, o, drain
-  static constexpr int MISC = BAR + 9 * 8;            // TMEM base, abort flag
-  static constexpr int BYTES = MISC + 16;
-  static constexpr int ALLOC = BYTES + 1024;          // slack for 1024-byte alignment
-};
-static_assert(Tc::ALLOC <= 227 * 1024, "fits an SM");
-
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
-
-template <typename T>
-__device__ __forceinline__ void store_pair(uint8_t* hi_at, uint8_t* lo_at, uint32_t o, float x, float y) {
-  uint32_t hi, lo;
-  split2<T>(x, y, hi, lo);
-  *reinterpret_cast<uint32_t*>(hi_at + o) = hi;
-  *reinterpret_cast<uint32_t*>(lo_at + o) = lo;
-}
-
-// X's blocks below the diagonal in columns [16 JB + 8 hf, + 8): X_ij = -X_ii sum_{k=j}^{i-1} L_ik X_kj.
-// L's blocks lie as two terms in lh / ll, X's in xh / xl (shared addresses of [64][64] tiles).
-template <typename T, int JB>
-__device__ __forceinline__ void off_diagonal(uint8_t* XH, uint8_t* XL, uint32_t lh, uint32_t ll, int hf, int lane) {
-  const int mi = lane >> 3, lr = lane & 7, gr = lane >> 2, cq = lane & 3;
-  const uint32_t xh = smem_u32(XH), xl = smem_u32(XL);
-  const int s0 = 16 * JB + 8 * hf;
-  uint32_t bh[4][2], bl[4][2];
-  ldmatrix_x2_trans(bh[JB], xh + piece<128>(16 * JB + (mi & 1) * 8 + lr, s0 >> 3));
-  ldmatrix_x2_trans(bl[JB], xl + piece<128>(16 * JB + (mi & 1) * 8 + lr, s0 >> 3));
-#pragma unroll
-  for (int i = JB + 1; i < 4; ++i) {
-    float y[4] = {}, x[4] = {};
-    uint32_t ah[4], al[4];
-#pragma unroll
-    for (int k = JB; k < i; ++k) {
-      const uint32_t o = piece<128>(16 * i + (mi & 1) * 8 + lr, 2 * k + (mi >> 1));
-      ldmatrix_x4(ah, lh + o);
-      ldmatrix_x4(al, ll + o);
-      mma_tile(T(), y, al, bh[k][0], bh[k][1]);
-      mma_tile(T(), y, ah, bl[k][0], bl[k][1]);
-      mma_tile(T(), y, ah, bh[k][0], bh[k][1]);
-    }
-    uint32_t h0, l0, h1, l1;
-    split2<T>(-y[0], -y[1], h0, l0);
-    split2<T>(-y[2], -y[3], h1, l1);
-    h0 = movmatrix_trans(h0);
-    h1 = movmatrix_trans(h1);
-    l0 = movmatrix_trans(l0);
-    l1 = movmatrix_trans(l1);
-    const uint32_t o = piece<128>(16 * i + (mi & 1) * 8 + lr, 2 * i + (mi >> 1));
-    ldmatrix_x4(ah, xh + o);
-    ldmatrix_x4(al, xl + o);
-    mma_tile(T(), x, al, h0, h1);
-    mma_tile(T(), x, ah, l0, l1);
-    mma_tile(T(), x, ah, h0, h1);
-    split2<T>(x[0], x[1], h0, l0);
-    split2<T>(x[2], x[3], h1, l1);
-    const uint32_t w0 = piece<128>(16 * i + gr, s0 >> 3) + 4 * cq, w1 = piece<128>(16 * i + gr + 8, s0 >> 3) + 4 * cq;
-    *reinterpret_cast<uint32_t*>(XH + w0) = h0;
-    *reinterpret_cast<uint32_t*>(XL + w0) = l0;
-    *reinterpret_cast<uint32_t*>(XH + w1) = h1;
-    *reinterpret_cast<uint32_t*>(XL + w1) = l1;
-    bh[i][0] = movmatrix_trans(h0);
-    bh[i][1] = movmatrix_trans(h1);
-    bl[i][0] = movmatrix_trans(l0);
-    bl[i][1] = movmatrix_trans(l1);
-  }
-}
-
-// The preparing warps: warp w owns tokens [16 w, 16 w + 16) of K K^T, Q K^T, L and M.
-template <typename T>
-__device__ void tc_prepare(const GdnFwd& p, uint8_t* sm, int h, int seq, int len, int tid, volatile int* abort_flag) {
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Tc::BAR);
-  uint64_t* used = full + 2;
-  const int w = tid >> 5, lane = tid & 31;
-  const int mi = lane >> 3, lr = lane & 7, gr = lane >> 2, cq = lane & 3;
-  const int kh = h / (p.n_v / p.n_k), n_chunks = (len + TC_C - 1) / TC_C;
-  const T* q = static_cast<const T*>(p.q) + seq * p.q_seq + kh * TC_D;
-  const T* k = static_cast<const T*>(p.k) + seq * p.k_seq + kh * TC_D;
-  const T* v = static_cast<const T*>(p.v) + seq * p.v_seq + h * TC_D;
-  const float* g = p.gb + (static_cast<int64_t>(seq) * 2 * p.n_v + h) * p.T;
-  const float* b = g + static_cast<int64_t>(p.n_v) * p.T;
-  const uint32_t base = smem_u32(sm);
-
-  // a thread copies 16-byte column tid % 16 of every 8th row; rows past the end are zero, never read
-  const int xc = tid & 15, r0 = tid >> 4;
-  auto load = [&](int c) {
-    const uint32_t st = base + (c % 3) * Tc::IN + (xc >> 3) * Tc::HALF;
-    const uint32_t sv = base + (c % 3) * Tc::IN + Tc::V + (xc >> 3) * Tc::TILE;
-    const int64_t t0 = static_cast<int64_t>(c) * TC_C + r0;
-    const T* kp = k + t0 * p.k_ld + 8 * xc;
-    const T* qp = q + t0 * p.q_ld + 8 * xc;
-    const T* vp = v + t0 * p.v_ld + 8 * xc;
-#pragma unroll
-    for (int i = 0; i < TC_C / 8; ++i) {
-      const bool on = t0 + 8 * i < len;
-      const uint32_t o = piece<128>(8 * i + r0, xc & 7);
-      cp_async16(st + Tc::K + o, on ? kp : k, on ? 16 : 0);
-      cp_async16(st + Tc::Q + o, on ? qp : q, on ? 16 : 0);
-      cp_async16(sv + o, on ? vp : v, on ? 16 : 0);
-      kp += 8 * p.k_ld;
-      qp += 8 * p.q_ld;
-      vp += 8 * p.v_ld;
-    }
-  };
-  // warp 0: gates of tokens 2 lane and 2 lane + 1
-  float g0n = 0.f, g1n = 0.f, b0n = 0.f, b1n = 0.f;
-  auto load_gates = [&](int c) {
-    const int64_t t = static_cast<int64_t>(c) * TC_C + 2 * lane;
-    g0n = t < len ? g[t] : 0.f;
-    b0n = t < len ? b[t] : 0.f;
-    g1n = t + 1 < len ? g[t + 1] : 0.f;
-    b1n = t + 1 < len ? b[t + 1] : 0.f;
-  };
-  if (n_chunks > 0) load(0);
-  cp_async_commit();
-  if (n_chunks > 1) load(1);
-  cp_async_commit();
-  if (w == 0) load_gates(0);
-  // the blocks above X's and M's diagonals stay zero
-  for (int i = tid; i < 2 * Tc::XM / 16; i += TC_PREP)
-    reinterpret_cast<uint4*>(sm + Tc::XH)[i] = make_uint4(0u, 0u, 0u, 0u);
-
-  float* gh = reinterpret_cast<float*>(sm + Tc::GAM);
-  float* glo = gh + TC_C;
-  float* bet = gh + 2 * TC_C;
-  for (int c = 0; c < n_chunks; ++c) {
-    uint8_t* XH = sm + Tc::XH + (c & 1) * Tc::XM;
-    uint8_t* XL = XH + Tc::TILE;
-    uint8_t* MH = XL + Tc::TILE;
-    uint8_t* ML = MH + Tc::TILE;
-    const uint32_t st = base + (c % 3) * Tc::IN;
-    if (w == 0) {
-      float ga = g0n, gb = g1n;
-      const float ba = b0n, bb = b1n;
-      load_gates(c + 1);  // (past the last chunk: zeros)
-      // e^g is 0 in fp32 from -104 on; the clamp keeps -infinity out of the differences
-      ga = ga < -1000.f ? -1000.f : ga;
-      gb = gb < -1000.f ? -1000.f : gb;
-      // cumulative decays as unevaluated sums of two floats (see above)
-      float s = ga + gb, r = s - ga, sl = (ga - (s - r)) + (gb - r);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_up_sync(0xffffffffu, s, o), yl = __shfl_up_sync(0xffffffffu, sl, o);
-        if (lane >= o) {
-          const float z = s + y;
-          r = z - s;
-          sl += yl + ((s - (z - r)) + (y - r));
-          s = z;
-        }
-      }
-      // token 2 lane: the pair's sum without its second gate
-      const float s1 = s - gb;
-      r = s1 - s;
-      const float s1l = sl + ((s - (s1 - r)) + (-gb - r));
-      const float last = __shfl_sync(0xffffffffu, s, 31), lastl = __shfl_sync(0xffffffffu, sl, 31);
-      reinterpret_cast<float2*>(gh)[lane] = make_float2(s1, s);
-      reinterpret_cast<float2*>(glo)[lane] = make_float2(s1l, sl);
-      reinterpret_cast<float2*>(bet)[lane] = make_float2(ba, bb);
-      float2* f = reinterpret_cast<float2*>(sm + Tc::SC + (c & 1) * Tc::SC_BYTES);
-      const float e0 = expf(s1 + s1l), e1 = expf(s + sl);
-      f[lane] = make_float2(e0, e1);
-      f[32 + lane] = make_float2(ba * e0, bb * e1);
-      f[64 + lane] = make_float2(ba, bb);
-      f[96 + lane] = make_float2(expf((last - s1) + (lastl - s1l)), expf((last - s) + (lastl - sl)));
-      if (lane == 0) f[128] = make_float2(expf(last + lastl), 0.f);
-    }
-    cp_async_wait<1>();
-    bar_sync(2, TC_PREP);  // the chunk's rows, gam and beta are there for every preparing warp
-    float kk[4][2][4] = {}, qk[4][2][4] = {};
-#pragma unroll
-    for (int ks = 0; ks < TC_D / 16; ++ks) {
-      const uint32_t half = st + (ks >> 2) * Tc::HALF;
-      const int pc = 2 * (ks & 3) + (mi >> 1), pr = (mi & 1) * 8 + lr;
-      uint32_t a[4], x[4], y[4];
-      ldmatrix_x4(a, half + Tc::K + piece<128>(16 * w + pr, pc));
-      ldmatrix_x4(x, half + Tc::Q + piece<128>(16 * w + pr, pc));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j > w) continue;  // (the same for the whole warp)
-        ldmatrix_x4(y, half + Tc::K + piece<128>(16 * j + pr, pc));
-        mma_n<T>(kk[j][0], kk[j][1], a, y);
-        mma_n<T>(qk[j][0], qk[j][1], x, y);
-      }
-    }
-    // L and M: e^(gam_t - gam_s) directly in the diagonal block, below it as a product around the last
-    // token of the block row before.  L's blocks below the diagonal wait in M's place
-    {
-      const int t0 = 16 * w + gr, t1 = t0 + 8;
-      const float h0 = gh[t0], h1 = gh[t1], l0 = glo[t0], l1 = glo[t1], b0 = bet[t0], b1 = bet[t1];
-      const float rh = w ? gh[16 * w - 1] : 0.f, rl = w ? glo[16 * w - 1] : 0.f;
-      const float rf0 = __expf((h0 - rh) + (l0 - rl)), rf1 = __expf((h1 - rh) + (l1 - rl));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j > w) continue;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int s = 16 * j + 8 * i + 2 * cq;
-          const float2 gs = *reinterpret_cast<const float2*>(gh + s), ls = *reinterpret_cast<const float2*>(glo + s);
-          float(&x)[4] = kk[j][i];
-          float(&m)[4] = qk[j][i];
-          if (j < w) {
-            const float c0 = __expf((rh - gs.x) + (rl - ls.x)), c1 = __expf((rh - gs.y) + (rl - ls.y));
-            m[0] *= rf0 * c0;
-            m[1] *= rf0 * c1;
-            m[2] *= rf1 * c0;
-            m[3] *= rf1 * c1;
-            store_pair<T>(MH, ML, piece<128>(t0, s >> 3) + 4 * cq, b0 * rf0 * c0 * x[0], b0 * rf0 * c1 * x[1]);
-            store_pair<T>(MH, ML, piece<128>(t1, s >> 3) + 4 * cq, b1 * rf1 * c0 * x[2], b1 * rf1 * c1 * x[3]);
-          } else {
-            const float d0 = __expf((h0 - gs.x) + (l0 - ls.x)), d1 = __expf((h0 - gs.y) + (l0 - ls.y));
-            const float d2 = __expf((h1 - gs.x) + (l1 - ls.x)), d3 = __expf((h1 - gs.y) + (l1 - ls.y));
-            uint8_t* ld = sm + Tc::LD + w * 16 * 64;
-            const int sc = s & 15;
-            *reinterpret_cast<float2*>(ld + piece_f(gr, sc >> 2) + (sc & 3) * 4) =
-                make_float2(s < t0 ? b0 * d0 * x[0] : 0.f, s + 1 < t0 ? b0 * d1 * x[1] : 0.f);
-            *reinterpret_cast<float2*>(ld + piece_f(gr + 8, sc >> 2) + (sc & 3) * 4) =
-                make_float2(s < t1 ? b1 * d2 * x[2] : 0.f, s + 1 < t1 ? b1 * d3 * x[3] : 0.f);
-            m[0] = s <= t0 ? d0 * m[0] : 0.f;
-            m[1] = s + 1 <= t0 ? d1 * m[1] : 0.f;
-            m[2] = s <= t1 ? d2 * m[2] : 0.f;
-            m[3] = s + 1 <= t1 ? d3 * m[3] : 0.f;
-          }
-        }
-      }
-    }
-    bar_sync(2, TC_PREP);
-    // the diagonal blocks of X = (I + L)^-1 in fp32, one row a thread: x (I + L) = e_r from the last
-    // column down (x_s is final when reached and leaves every earlier column)
-    if (tid < 64) {
-      const int r = tid & 15, blk = tid >> 4;
-      const uint8_t* ld = sm + Tc::LD + blk * 16 * 64;
-      float x[16];
-#pragma unroll
-      for (int s = 0; s < 16; ++s) x[s] = s == r ? 1.f : 0.f;
-#pragma unroll
-      for (int s = 15; s >= 1; --s) {
-        float l[16];
-#pragma unroll
-        for (int i = 0; i < s; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(ld + piece_f(s, i >> 2));
-          l[i] = f.x;
-          l[i + 1] = f.y;
-          l[i + 2] = f.z;
-          l[i + 3] = f.w;
-        }
-#pragma unroll
-        for (int i = 0; i < s; ++i) x[i] = fmaf(-x[s], l[i], x[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) split2<T>(x[8 * i + 2 * j], x[8 * i + 2 * j + 1], hi[j], lo[j]);
-        const uint32_t o = piece<128>(16 * blk + r, 2 * blk + i);
-        *reinterpret_cast<uint4*>(XH + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(XL + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-    }
-    bar_sync(2, TC_PREP);
-    const uint32_t lh = smem_u32(MH), ll = smem_u32(ML);
-    if (w < 2) {
-      off_diagonal<T, 0>(XH, XL, lh, ll, w, lane);
-    } else {
-      off_diagonal<T, 1>(XH, XL, lh, ll, w - 2, lane);
-      off_diagonal<T, 2>(XH, XL, lh, ll, w - 2, lane);
-    }
-    bar_sync(2, TC_PREP);  // L is read: M takes its place
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j > w) continue;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int pc = 2 * j + i;
-        store_pair<T>(MH, ML, piece<128>(16 * w + gr, pc) + 4 * cq, qk[j][i][0], qk[j][i][1]);
-        store_pair<T>(MH, ML, piece<128>(16 * w + gr + 8, pc) + 4 * cq, qk[j][i][2], qk[j][i][3]);
-      }
-    }
-    fence_proxy_async_smem();  // rows, X and M are read by the tensor cores
-    bar_sync(2, TC_PREP);
-    if (tid == 0) mbar_arrive(&full[c & 1]);
-    // chunk c - 1 is consumed: its rows' place takes chunk c + 2, its X and M's place the next chunk's
-    if (c >= 1 && c + 1 < n_chunks && !*abort_flag &&
-        !mbar_wait(&used[(c - 1) & 1], ((c - 1) >> 1) & 1, abort_flag)) {
-      *abort_flag = 1;
-      set_device_error(p.err, KVA_DEV_WAIT_TIMEOUT);
-    }
-    if (c + 2 < n_chunks) load(c + 2);
-    cp_async_commit();
-  }
-  cp_async_wait<0>();
-}
-
-// A wait of the main warps; on giving up, the flag ends every other wait of the block too.
-__device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
-  if (*abort_flag) return;
-  if (!mbar_wait(bar, parity, abort_flag)) {
-    *abort_flag = 1;
-    set_device_error(err, KVA_DEV_WAIT_TIMEOUT);
-  }
-}
-
-template <typename T>
-__device__ void tc_main(const GdnFwd& p, uint8_t* sm, int h, int seq, int len, int tid, uint32_t tb,
-                        volatile int* abort_flag) {
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Tc::BAR);
-  uint64_t *used = full + 2, *ybar = full + 4, *ubar = full + 5, *sbar = full + 6, *obar = full + 7, *drain = full + 8;
-  const int warp = tid >> 5, lane = tid & 31, qd = warp & 3, hc = warp >> 2;
-  const int row = 32 * qd + lane, n_chunks = (len + TC_C - 1) / TC_C;
-  const uint32_t tl = tb + (static_cast<uint32_t>(32 * qd) << 16);
-  const int64_t srow = ((static_cast<int64_t>(seq) * p.n_v + h) * TC_D + row) * TC_D + 64 * hc;
-  T* out = static_cast<T*>(p.out) + seq * p.out_seq + h * TC_D + row;
-  constexpr uint32_t FMT = F16<T>::umma_fmt;
-  constexpr uint32_t ID_128 = idesc_f16kind_f32_major(128, 128, FMT, false, false);
-  constexpr uint32_t ID_64 = idesc_f16kind_f32_major(128, 64, FMT, false, false);
-  constexpr uint32_t ID_S = idesc_f16kind_f32_major(128, 128, FMT, false, true);
-
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    uint32_t r[32];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float4 x = reinterpret_cast<const float4*>(p.state_in + srow + 32 * i)[j];
-      r[4 * j] = __float_as_uint(x.x);
-      r[4 * j + 1] = __float_as_uint(x.y);
-      r[4 * j + 2] = __float_as_uint(x.z);
-      r[4 * j + 3] = __float_as_uint(x.w);
-    }
-    tmem_st_32x32b_x32(tl + TM_S + 64 * hc + 32 * i, r);
-  }
-  tmem_st_wait();
-
-  // warp 0's issuing lane, elected once: a commit tracks only its own lane's MMAs
-  const uint32_t issuer = warp == 0 ? elect_one() : 0u;
-  float zr[32];
-  // the readout of chunk c, this thread's 32 tokens: Z (in zr) + O
-  auto write_out = [&](int c) {
-    tc_wait(obar, c & 1, abort_flag, p.err);
-    tc_fence_after();
-    uint32_t r[32];
-    tmem_ld_32x32b_x32(tl + TM_O + 32 * hc, r);
-    tmem_ld_wait();
-    const int64_t t0 = static_cast<int64_t>(c) * TC_C + 32 * hc;
-    T* o = out + t0 * p.out_ld;
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (t0 + j < len) o[j * p.out_ld] = F16<T>::from(p.scale * (zr[j] + u2f(r[j])));
-  };
-
-  for (int c = 0; c < n_chunks; ++c) {
-    const uint8_t* in = sm + (c % 3) * Tc::IN;
-    const float* sc = reinterpret_cast<const float*>(sm + Tc::SC + (c & 1) * Tc::SC_BYTES);
-    const uint32_t kq = smem_u32(in), xh = smem_u32(sm + Tc::XH + (c & 1) * Tc::XM);
-    tc_wait(&full[c & 1], (c >> 1) & 1, abort_flag, p.err);
-    if (c > 0) tc_wait(sbar, (c - 1) & 1, abort_flag, p.err);
-    tc_fence_after();
-    // pass 1
-    {
-      const float gl = sc[4 * TC_C];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t r[32], hi[16], lo[16];
-        tmem_ld_32x32b_x32(tl + TM_S + 64 * hc + 32 * i, r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) split2<T>(u2f(r[2 * j]), u2f(r[2 * j + 1]), hi[j], lo[j]);
-        tmem_st_32x32b_x16(tl + TM_A + 32 * hc + 16 * i, hi);
-        tmem_st_32x32b_x16(tl + TM_A + 64 + 32 * hc + 16 * i, lo);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(gl * u2f(r[j]));
-        tmem_st_32x32b_x32(tl + TM_S + 64 * hc + 32 * i, r);
-      }
-    }
-    tmem_st_wait();
-    // (Y's columns held the readout's operand: its MMAs are through before Y is written again)
-    if (c > 0) tc_wait(obar, (c - 1) & 1, abort_flag, p.err);
-    tc_fence_before();
-    bar_sync(1, TC_MAIN);
-    if (warp == 0) {
-      tc_fence_after();
-      if (issuer && !*abort_flag) {
-        const uint64_t d = sdesc_k_sw128(kq);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          umma_f16_ts(tb + TM_Y, tb + TM_A + 8 * j, d + (((j >> 2) * Tc::HALF + (j & 3) * 32) >> 4), ID_128, j > 0);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          umma_f16_ts(tb + TM_Y, tb + TM_A + 64 + 8 * j, d + (((j >> 2) * Tc::HALF + (j & 3) * 32) >> 4), ID_64, 1);
-        umma_commit(ybar);
-      }
-      __syncwarp();
-    }
-    if (c > 0) write_out(c - 1);
-    tc_wait(ybar, c & 1, abort_flag, p.err);
-    tc_fence_after();
-    // pass 2
-    {
-      uint32_t r[32], hi[16], lo[16];
-      tmem_ld_32x32b_x32(tl + TM_Y + 32 * hc, r);
-      const uint8_t* vt = in + Tc::V + (row >> 6) * Tc::TILE;
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int t = 32 * hc + 2 * j;
-        const float2 eb = *reinterpret_cast<const float2*>(sc + TC_C + t);
-        const float2 be = *reinterpret_cast<const float2*>(sc + 2 * TC_C + t);
-        const T v0 = *reinterpret_cast<const T*>(vt + piece<128>(t, (row & 63) >> 3) + (row & 7) * 2);
-        const T v1 = *reinterpret_cast<const T*>(vt + piece<128>(t + 1, (row & 63) >> 3) + (row & 7) * 2);
-        split2<T>(fmaf(-eb.x, u2f(r[2 * j]), be.x * F16<T>::to(v0)), fmaf(-eb.y, u2f(r[2 * j + 1]), be.y * F16<T>::to(v1)),
-                  hi[j], lo[j]);
-      }
-      tmem_st_32x32b_x16(tl + TM_A + 16 * hc, hi);
-      tmem_st_32x32b_x16(tl + TM_A + 32 + 16 * hc, lo);
-    }
-    tmem_st_wait();
-    tc_fence_before();
-    bar_sync(1, TC_MAIN);
-    if (warp == 0) {
-      tc_fence_after();
-      if (issuer && !*abort_flag) {
-        const uint64_t dh = sdesc_k_sw128(xh), dl = sdesc_k_sw128(xh + Tc::TILE);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_U, tb + TM_A + 32 + 8 * j, dh + 2 * j, ID_64, j > 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_U, tb + TM_A + 8 * j, dl + 2 * j, ID_64, 1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_U, tb + TM_A + 8 * j, dh + 2 * j, ID_64, 1);
-        umma_commit(ubar);
-      }
-      __syncwarp();
-    }
-    {
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(tl + TM_Z + 32 * hc, r);
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 32; ++j) zr[j] = sc[32 * hc + j] * u2f(r[j]);
-    }
-    tc_wait(ubar, c & 1, abort_flag, p.err);
-    tc_fence_after();
-    // pass 3
-    {
-      uint32_t r[32], hi[16], lo[16];
-      tmem_ld_32x32b_x32(tl + TM_U + 32 * hc, r);
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float2 e = *reinterpret_cast<const float2*>(sc + 3 * TC_C + 32 * hc + 2 * j);
-        split2<T>(e.x * u2f(r[2 * j]), e.y * u2f(r[2 * j + 1]), hi[j], lo[j]);
-      }
-      tmem_st_32x32b_x16(tl + TM_A + 16 * hc, hi);
-      tmem_st_32x32b_x16(tl + TM_A + 32 + 16 * hc, lo);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) split2<T>(u2f(r[2 * j]), u2f(r[2 * j + 1]), hi[j], lo[j]);
-      tmem_st_32x32b_x16(tl + TM_Y + 16 * hc, hi);
-      tmem_st_32x32b_x16(tl + TM_Y + 32 + 16 * hc, lo);
-    }
-    tmem_st_wait();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&used[c & 1]);  // this warp is through with V and the scalars
-    bar_sync(1, TC_MAIN);
-    if (warp == 0) {
-      tc_fence_after();
-      if (issuer && !*abort_flag) {
-        const uint64_t dk = sdesc_mn_sw128(kq, Tc::HALF);
-        const uint64_t mh = sdesc_k_sw128(xh + 2 * Tc::TILE), ml = sdesc_k_sw128(xh + 3 * Tc::TILE);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_S, tb + TM_A + 32 + 8 * j, dk + ((j * 2048) >> 4), ID_S, 1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_S, tb + TM_A + 8 * j, dk + ((j * 2048) >> 4), ID_S, 1);
-        umma_commit(sbar);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_O, tb + TM_Y + 32 + 8 * j, mh + 2 * j, ID_64, j > 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_O, tb + TM_Y + 8 * j, ml + 2 * j, ID_64, 1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) umma_f16_ts(tb + TM_O, tb + TM_Y + 8 * j, mh + 2 * j, ID_64, 1);
-        umma_commit(obar);
-        umma_commit(&used[c & 1]);
-      }
-      __syncwarp();
-    }
-  }
-  if (n_chunks > 0) {
-    write_out(n_chunks - 1);
-    tc_wait(sbar, (n_chunks - 1) & 1, abort_flag, p.err);
-    tc_fence_after();
-  }
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    uint32_t r[32];
-    tmem_ld_32x32b_x32(tl + TM_S + 64 * hc + 32 * i, r);
-    tmem_ld_wait();
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      reinterpret_cast<float4*>(p.state_out + srow + 32 * i)[j] =
-          make_float4(u2f(r[4 * j]), u2f(r[4 * j + 1]), u2f(r[4 * j + 2]), u2f(r[4 * j + 3]));
-  }
-  if (warp == 0) {  // every MMA this block issued has landed before it frees the tensor memory
-    if (issuer) {
-      umma_commit(drain);
-      if (!mbar_wait_limit(drain, 0)) set_device_error(p.err, KVA_DEV_WAIT_TIMEOUT);
-    }
-    __syncwarp();
-  }
-}
-
-// grid (n_v, n_seq), one block an SM (its tensor memory and 223 KB of its shared memory)
-template <typename T>
-__global__ void __launch_bounds__(TC_MAIN + TC_PREP, 1) gdn_tc_kernel(const __grid_constant__ GdnFwd p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Tc::BAR);
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Tc::MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Tc::MISC + 4);
-  const int tid = threadIdx.x;
-  if (tid == 0) {
-    for (int i = 0; i < 9; ++i) mbar_init(&bars[i], i == 2 || i == 3 ? 1 + TC_MAIN / 32 : 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (tid < 32) {
-    tmem_alloc(tslot, TM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tb = *tslot;
-  griddep_wait_and_release();
-  const int seq = blockIdx.y, len = p.has_lens ? p.lens[seq] : p.T;
-  if (tid < TC_MAIN) tc_main<T>(p, sm, blockIdx.x, seq, len, tid, tb, abort_flag);
-  else tc_prepare<T>(p, sm, blockIdx.x, seq, len, tid - TC_MAIN, abort_flag);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (tid < 32) tmem_dealloc(tb, TM_COLS);
-}
-
 template <typename T, int D>
 cudaError_t launch(const GdnFwd& p, int n_seq, int longest, cudaStream_t s) {
   if (longest <= kStepTokens)
     return launch_pdl(gdn_recurrent_kernel<T, D>, dim3(p.n_v * (D / 32), n_seq), dim3(256), 0, s, p);
-  if constexpr (D == TC_D) {
-    if (longest >= kTcTokens) {
-      const cudaError_t e = cudaFuncSetAttribute(gdn_tc_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc::ALLOC);
-      if (e != cudaSuccess) return e;
-      return launch_pdl(gdn_tc_kernel<T>, dim3(p.n_v, n_seq), dim3(TC_MAIN + TC_PREP), Tc::ALLOC, s, p);
-    }
-  }
   const cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              Chunk<D>::BYTES);
   if (e != cudaSuccess) return e;
