@@ -119,10 +119,8 @@ __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constan
 constexpr int CH = 16;          // tokens a run
 constexpr int ROWS = 64;        // state rows a block
 constexpr int CHAIN = ROWS / 16;  // chain warps
-constexpr int PREP = 2;         // preparing warps: runs of their own parity
-constexpr int AHEAD = 2;        // a preparing warp's runs in flight behind the one it works on
+constexpr int LOADED = 4;       // runs in flight behind those being prepared
 constexpr int NST = 8;          // stages: the run of AHEAD + 1 own steps back is consumed when its place is needed
-constexpr int kChunkThreads = 32 * (CHAIN + PREP);
 
 template <int D>
 struct Stage {
@@ -142,7 +140,7 @@ struct Prep {                                      // per preparing warp: L in f
   static constexpr int LDL = 20;
   static constexpr int BYTES = (CH * LDL + CH) * 4;
 };
-template <int D>
+template <int D, int PREP>
 struct Chunk {
   static constexpr int L = NST * Stage<D>::BYTES;
   static constexpr int BAR = L + PREP * Prep::BYTES;  // full[NST], empty[NST]
@@ -161,12 +159,29 @@ __device__ __forceinline__ uint32_t piece16(int r, int c) {
   return static_cast<uint32_t>(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
 }
 
+// two fp32 operations an instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {  // a - b: b times -1 is exact
+  float2 d, m1 = make_float2(-1.f, -1.f);
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(b)), "l"(reinterpret_cast<unsigned long long&>(m1)),
+        "l"(reinterpret_cast<unsigned long long&>(a)));
+  return d;
+}
+
 // x as two 16-bit terms: hi + lo holds x to the square of the type's half step
 template <typename T>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = F16<T>::pack(x, y);
-  const float2 h = F16<T>::unpack(hi);
-  lo = F16<T>::pack(x - h.x, y - h.y);
+  const float2 l = sub2(make_float2(x, y), F16<T>::unpack(hi));
+  lo = F16<T>::pack(l.x, l.y);
 }
 // accumulator fragments of two neighbouring 8-column tiles as an A operand (16 x 16)
 template <typename T>
@@ -195,11 +210,13 @@ __device__ __forceinline__ void mma2(float (&d0)[4], float (&d1)[4], const uint3
   mma_tile(T(), d1, a, b[i2], b[i3]);
 }
 
-template <typename T, int D>
+// A preparing warp: runs pw, pw + PREP, ...
+template <typename T, int D, int PREP>
 __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int seq, int len, int pw, int lane,
                              volatile int* abort_flag) {
   using St = Stage<D>;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Chunk<D>::BAR);
+  constexpr int AHEAD = LOADED / PREP;  // own runs in flight behind the one worked on
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Chunk<D, PREP>::BAR);
   uint64_t* empty = full + NST;
   const int kh = h / (p.n_v / p.n_k), n_runs = (len + CH - 1) / CH;
   const T* q = static_cast<const T*>(p.q) + seq * p.q_seq + kh * D;
@@ -207,7 +224,7 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
   const T* v = static_cast<const T*>(p.v) + seq * p.v_seq + h * D + half * ROWS;
   const float* g = p.gb + (static_cast<int64_t>(seq) * 2 * p.n_v + h) * p.T;
   const float* b = g + static_cast<int64_t>(p.n_v) * p.T;
-  float* Ls = reinterpret_cast<float*>(sm + Chunk<D>::L + pw * Prep::BYTES);
+  float* Ls = reinterpret_cast<float*>(sm + Chunk<D, PREP>::L + pw * Prep::BYTES);
   const uint32_t base = smem_u32(sm);
 
   // a lane copies one 16-byte column of every RK-th (V: RV-th) row of a run
@@ -385,11 +402,11 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
   cp_async_wait<0>();
 }
 
-template <typename T, int D>
+template <typename T, int D, int PREP>
 __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int seq, int len, int warp, int lane,
                            volatile int* abort_flag) {
   using St = Stage<D>;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Chunk<D>::BAR);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Chunk<D, PREP>::BAR);
   uint64_t* empty = full + NST;
   const int n_runs = (len + CH - 1) / CH;
   const int mi = lane >> 3, lr = lane & 7, gr = lane >> 2, cq = lane & 3;
@@ -483,7 +500,11 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S[j][e] *= gl;
+      for (int e = 0; e < 4; e += 2) {
+        const float2 x = mul2(make_float2(S[j][e], S[j][e + 1]), make_float2(gl, gl));
+        S[j][e] = x.x;
+        S[j][e + 1] = x.y;
+      }
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint32_t kt[4];
@@ -520,12 +541,12 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
   }
 }
 
-// grid (n_v * D / 64, n_seq): 64 state rows of one head, four chain warps and two preparing ones
-template <typename T, int D>
-__global__ void __launch_bounds__(kChunkThreads, 2) gdn_chunk_kernel(const __grid_constant__ GdnFwd p) {
+// grid (n_v * D / 64, n_seq): 64 state rows of one head, four chain warps and PREP preparing ones
+template <typename T, int D, int PREP, int BLOCKS>
+__global__ void __launch_bounds__(32 * (CHAIN + PREP), BLOCKS) gdn_chunk_kernel(const __grid_constant__ GdnFwd p) {
   extern __shared__ __align__(128) uint8_t sm[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Chunk<D>::BAR);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Chunk<D>::MISC);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Chunk<D, PREP>::BAR);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Chunk<D, PREP>::MISC);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int HALVES = D / ROWS;
   const int h = blockIdx.x / HALVES, half = blockIdx.x % HALVES, seq = blockIdx.y;
@@ -540,18 +561,26 @@ __global__ void __launch_bounds__(kChunkThreads, 2) gdn_chunk_kernel(const __gri
   __syncthreads();
   griddep_wait_and_release();
   const int len = p.has_lens ? p.lens[seq] : p.T;
-  if (warp < CHAIN) chain_runs<T, D>(p, sm, h, half, seq, len, warp, lane, abort_flag);
-  else prepare_runs<T, D>(p, sm, h, half, seq, len, warp - CHAIN, lane, abort_flag);
+  if (warp < CHAIN) chain_runs<T, D, PREP>(p, sm, h, half, seq, len, warp, lane, abort_flag);
+  else prepare_runs<T, D, PREP>(p, sm, h, half, seq, len, warp - CHAIN, lane, abort_flag);
+}
+
+template <typename T, int D, int PREP, int BLOCKS>
+cudaError_t launch_chunk(const GdnFwd& p, dim3 grid, cudaStream_t s) {
+  auto kern = gdn_chunk_kernel<T, D, PREP, BLOCKS>;
+  constexpr int bytes = Chunk<D, PREP>::BYTES;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, grid, dim3(32 * (CHAIN + PREP)), bytes, s, p);
 }
 
 template <typename T, int D>
 cudaError_t launch(const GdnFwd& p, int n_seq, int longest, cudaStream_t s) {
   if (longest <= kStepTokens)
     return launch_pdl(gdn_recurrent_kernel<T, D>, dim3(p.n_v * (D / 32), n_seq), dim3(256), 0, s, p);
-  const cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Chunk<D>::BYTES);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(gdn_chunk_kernel<T, D>, dim3(p.n_v * (D / ROWS), n_seq), dim3(kChunkThreads), Chunk<D>::BYTES, s, p);
+  const dim3 grid(p.n_v * (D / ROWS), n_seq);
+  if (static_cast<int64_t>(grid.x) * grid.y <= num_sms()) return launch_chunk<T, D, 4, 1>(p, grid, s);
+  return launch_chunk<T, D, 2, 2>(p, grid, s);
 }
 
 bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
