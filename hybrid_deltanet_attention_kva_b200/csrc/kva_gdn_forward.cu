@@ -28,15 +28,30 @@ struct GdnFwd {
 // runs of at most this many tokens go token by token
 constexpr int kStepTokens = 8;
 
-// 4 consecutive 16-bit values as floats
-template <typename T>
-__device__ __forceinline__ void load4(float (&f)[4], const T* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  const float2 a = F16<T>::unpack(u.x), b = F16<T>::unpack(u.y);
-  f[0] = a.x;
-  f[1] = a.y;
-  f[2] = b.x;
-  f[3] = b.y;
+// two fp32 operations an instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {  // a - b: b times -1 is exact
+  float2 d, m1 = make_float2(-1.f, -1.f);
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(b)), "l"(reinterpret_cast<unsigned long long&>(m1)),
+        "l"(reinterpret_cast<unsigned long long&>(a)));
+  return d;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
 }
 __device__ __forceinline__ float sum8(float v) {  // over the 8 lanes of a row
   v += __shfl_xor_sync(0xffffffffu, v, 4);
@@ -45,63 +60,100 @@ __device__ __forceinline__ float sum8(float v) {  // over the 8 lanes of a row
   return v;
 }
 
-// Token by token.  8 lanes hold a state row in fp32 registers (lane l the columns
-// 32 i + 4 l + j), a block of 256 threads 32 rows; grid (n_v * D / 32, n_seq).
-template <typename T, int D>
+// Token by token, for at most kStepTokens tokens.  8 lanes hold a state row in fp32 registers (lane l
+// the columns 32 i + 4 l + j); a block of 256 threads takes 32 RPT rows, RPT a thread, so its k, q, v and
+// gates are read once, together with the state, into shared memory.  HBM bounds it (the state is read
+// and written once).  grid (n_v * D / (32 RPT), n_seq)
+template <typename T, int D, int RPT>
 __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constant__ GdnFwd p) {
-  constexpr int NI = D / 32;
+  constexpr int NI = D / 32, ROWS = 32 * RPT, PARTS = D / ROWS, PC = D / 8;
+  __shared__ __align__(16) T ks[kStepTokens * D], qs[kStepTokens * D], vs[kStepTokens * ROWS];
+  __shared__ float ds[kStepTokens], bs[kStepTokens];
   griddep_wait_and_release();
-  const int h = blockIdx.x / NI, seq = blockIdx.y;
-  const int row = (blockIdx.x % NI) * 32 + (threadIdx.x >> 3), l = threadIdx.x & 7;
+  const int tid = threadIdx.x, h = blockIdx.x / PARTS, seq = blockIdx.y, r0 = (blockIdx.x % PARTS) * ROWS;
+  const int row = tid >> 3, l = tid & 7;
   const int kh = h / (p.n_v / p.n_k);
   const int len = p.has_lens ? p.lens[seq] : p.T;
-  const int64_t srow = ((static_cast<int64_t>(seq) * p.n_v + h) * D + row) * D + 4 * l;
-  const T* q = static_cast<const T*>(p.q) + seq * p.q_seq + kh * D + 4 * l;
-  const T* k = static_cast<const T*>(p.k) + seq * p.k_seq + kh * D + 4 * l;
-  const T* v = static_cast<const T*>(p.v) + seq * p.v_seq + h * D + row;
-  T* out = static_cast<T*>(p.out) + seq * p.out_seq + h * D + row;
-  const float* g = p.gb + (static_cast<int64_t>(seq) * 2 * p.n_v + h) * p.T;
-  const float* b = g + static_cast<int64_t>(p.n_v) * p.T;
+  const int64_t srow = ((static_cast<int64_t>(seq) * p.n_v + h) * D + r0 + row) * D + 4 * l;
 
-  float s[NI][4];
+  float2 s[RPT][NI][2];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const float4 x = *reinterpret_cast<const float4*>(p.state_in + srow + 32 * i);
-    s[i][0] = x.x;
-    s[i][1] = x.y;
-    s[i][2] = x.z;
-    s[i][3] = x.w;
+  for (int a = 0; a < RPT; ++a)
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(p.state_in + srow + a * 32 * D + 32 * i));
+      s[a][i][0] = make_float2(x.x, x.y);
+      s[a][i][1] = make_float2(x.z, x.w);
+    }
+  for (int x = tid; x < len * PC; x += 256) {
+    const int t = x / PC, c = x % PC * 8;
+    *reinterpret_cast<uint4*>(ks + t * D + c) =
+        *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + seq * p.k_seq + t * p.k_ld + kh * D + c);
+    *reinterpret_cast<uint4*>(qs + t * D + c) =
+        *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + seq * p.q_seq + t * p.q_ld + kh * D + c);
   }
+  for (int x = tid; x < len * (ROWS / 8); x += 256) {
+    const int t = x / (ROWS / 8), c = x % (ROWS / 8) * 8;
+    *reinterpret_cast<uint4*>(vs + t * ROWS + c) =
+        *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + seq * p.v_seq + t * p.v_ld + h * D + r0 + c);
+  }
+  if (tid < len) {
+    const float* g = p.gb + (static_cast<int64_t>(seq) * 2 * p.n_v + h) * p.T + tid;
+    ds[tid] = expf(*g);
+    bs[tid] = g[static_cast<int64_t>(p.n_v) * p.T];
+  }
+  __syncthreads();
+  T* out = static_cast<T*>(p.out) + seq * p.out_seq + h * D + r0 + row;
   for (int t = 0; t < len; ++t) {
-    const float dec = expf(g[t]);
-    float kk[NI][4], sk = 0.f;
+    const float2 dec = make_float2(ds[t], ds[t]);
+    const float beta = bs[t];
+    float2 kk[NI][2], sk[RPT];
+#pragma unroll
+    for (int a = 0; a < RPT; ++a) sk[a] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      load4<T>(kk[i], k + t * p.k_ld + 32 * i);
+      const uint2 u = *reinterpret_cast<const uint2*>(ks + t * D + 32 * i + 4 * l);
+      kk[i][0] = F16<T>::unpack(u.x);
+      kk[i][1] = F16<T>::unpack(u.y);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] *= dec;
-        sk = fmaf(s[i][j], kk[i][j], sk);
-      }
+      for (int a = 0; a < RPT; ++a)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[a][i][e] = mul2(s[a][i][e], dec);
+          sk[a] = fma2(s[a][i][e], kk[i][e], sk[a]);
+        }
     }
-    const float u = b[t] * (F16<T>::to(v[t * p.v_ld]) - sum8(sk));
-    float o = 0.f;
+    float2 o[RPT], u2[RPT];
+#pragma unroll
+    for (int a = 0; a < RPT; ++a) {
+      const float u = beta * (F16<T>::to(vs[t * ROWS + a * 32 + row]) - sum8(sk[a].x + sk[a].y));
+      u2[a] = make_float2(u, u);
+      o[a] = make_float2(0.f, 0.f);
+    }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      float qq[4];
-      load4<T>(qq, q + t * p.q_ld + 32 * i);
+      const uint2 u = *reinterpret_cast<const uint2*>(qs + t * D + 32 * i + 4 * l);
+      const float2 q0 = F16<T>::unpack(u.x), q1 = F16<T>::unpack(u.y);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] = fmaf(u, kk[i][j], s[i][j]);
-        o = fmaf(s[i][j], qq[j], o);
+      for (int a = 0; a < RPT; ++a) {
+        s[a][i][0] = fma2(u2[a], kk[i][0], s[a][i][0]);
+        s[a][i][1] = fma2(u2[a], kk[i][1], s[a][i][1]);
+        o[a] = fma2(s[a][i][0], q0, o[a]);
+        o[a] = fma2(s[a][i][1], q1, o[a]);
       }
     }
-    o = sum8(o);
-    if (l == 0) out[t * p.out_ld] = F16<T>::from(p.scale * o);
+#pragma unroll
+    for (int a = 0; a < RPT; ++a) {
+      const float r = sum8(o[a].x + o[a].y);
+      if (l == 0) out[t * p.out_ld + a * 32] = F16<T>::from(p.scale * r);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
-    *reinterpret_cast<float4*>(p.state_out + srow + 32 * i) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+  for (int a = 0; a < RPT; ++a)
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      __stcs(reinterpret_cast<float4*>(p.state_out + srow + a * 32 * D + 32 * i),
+             make_float4(s[a][i][0].x, s[a][i][0].y, s[a][i][1].x, s[a][i][1].y));
 }
 
 // ============================================================================
@@ -157,23 +209,6 @@ __device__ __forceinline__ uint32_t piece(int r, int c) {
 // the same in a [16][16] 16-bit tile (32-byte rows)
 __device__ __forceinline__ uint32_t piece16(int r, int c) {
   return static_cast<uint32_t>(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
-}
-
-// two fp32 operations an instruction
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-  return d;
-}
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) {  // a - b: b times -1 is exact
-  float2 d, m1 = make_float2(-1.f, -1.f);
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(b)), "l"(reinterpret_cast<unsigned long long&>(m1)),
-        "l"(reinterpret_cast<unsigned long long&>(a)));
-  return d;
 }
 
 // x as two 16-bit terms: hi + lo holds x to the square of the type's half step
@@ -576,9 +611,13 @@ cudaError_t launch_chunk(const GdnFwd& p, dim3 grid, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t launch(const GdnFwd& p, int n_seq, int longest, cudaStream_t s) {
-  if (longest <= kStepTokens)
-    return launch_pdl(gdn_recurrent_kernel<T, D>, dim3(p.n_v * (D / 32), n_seq), dim3(256), 0, s, p);
   const dim3 grid(p.n_v * (D / ROWS), n_seq);
+  if (longest <= kStepTokens) {
+    // two rows a thread where that still leaves four blocks an SM
+    if (static_cast<int64_t>(grid.x) * grid.y >= 4 * num_sms())
+      return launch_pdl(gdn_recurrent_kernel<T, D, 2>, grid, dim3(256), 0, s, p);
+    return launch_pdl(gdn_recurrent_kernel<T, D, 1>, dim3(p.n_v * (D / 32), n_seq), dim3(256), 0, s, p);
+  }
   if (static_cast<int64_t>(grid.x) * grid.y <= num_sms()) return launch_chunk<T, D, 4, 1>(p, grid, s);
   return launch_chunk<T, D, 2, 2>(p, grid, s);
 }
