@@ -494,7 +494,7 @@ extern "C" int kva_op_token_logprobs(const void* logits, int32_t dtype, int64_t 
   using namespace kva;
   if (rows < 0 || n_vocab <= 0 || n_top < 0) return KVA_ERR_INVALID_ARG;
   if (dtype != KVA_BF16 && dtype != KVA_F16 && dtype != KVA_F32) return KVA_ERR_INVALID_ARG;
-  if (n_top > KVA_LOGPROB_MAX_TOP) return KVA_ERR_TOO_LARGE;
+  if (n_top > KVA_LOGPROB_MAX_TOP || n_vocab > (1 << 30)) return KVA_ERR_TOO_LARGE;
   if (rows == 0) return KVA_OK;
   if (!logits || ld < n_vocab || (tokens != nullptr) != (logprob != nullptr)) return KVA_ERR_INVALID_ARG;
   if (n_top > 0 && (!top_id || !top_logprob)) return KVA_ERR_INVALID_ARG;

@@ -118,7 +118,12 @@ int kva_op_gdn_scan(const void* k, const void* v, const float* gb, float* state,
  *   u_t = beta_t (v_t - e^(g_t) S_(t-1) k_t)
  *   S_t = e^(g_t) S_(t-1) + u_t k_t^T          (= the recurrence of kva_op_gdn_scan)
  *   o_t = scale * S_t q_t
- * v head h reads k and q head h / (n_v / n_k).  The state is held in fp32 throughout. */
+ * v head h reads k and q head h / (n_v / n_k).  The state is held in fp32 throughout.
+ * Up to 8 tokens run one after the other in fp32; longer sequences in runs of 16 on the tensor
+ * cores, where fp32 operands enter as the sum of two values of `dtype` (an error of 2^-22
+ * relative with KVA_F16, 2^-16 with KVA_BF16; the state's part of a readout as one value).  With
+ * KVA_F16 the state and v - S k must then stay below 65504.  A NaN or an infinity in a token's
+ * inputs can reach the tokens of its run before it too. */
 typedef struct kva_gdn_forward_args {
   int32_t dtype;          /* 16-bit format of q, k, v and out: KVA_BF16 or KVA_F16 */
   int32_t n_seq;          /* sequences, 0..KVA_GDN_MAX_SEQ */
@@ -137,7 +142,8 @@ typedef struct kva_gdn_forward_args {
                              overlaps no input */
   int64_t out_ld, out_seq;
   const int32_t* lens;    /* HOST [n_seq] tokens of each sequence (0..T), or NULL: all T.  Tokens
-                             past a sequence's length are neither read nor written. */
+                             past a sequence's length are neither read nor written.  Read during
+                             the call: a captured graph keeps the lengths it was captured with. */
   float scale;            /* factor of the readout */
 } kva_gdn_forward_args;
 int kva_op_gdn_forward(const kva_gdn_forward_args* a, int32_t* err, void* stream);
@@ -147,7 +153,7 @@ int kva_op_gdn_forward(const kva_gdn_forward_args* a, int32_t* err, void* stream
  *   h_out[r] = h[r] + x[r], rounded to h_dtype
  *   y[r]     = h_out[r] / sqrt(mean(h_out[r]^2) + eps) * g
  * x [rows, ldx] in x_dtype, h and h_out [rows, ldh] in h_dtype (KVA_BF16, KVA_F16 or
- * KVA_F32); h_out may be h (in place), no other overlap.  y goes to out [rows, ldo]:
+ * KVA_F32); h_out may be h (in place), no other buffers overlap.  y goes to out [rows, ldo]:
  *   out_dtype KVA_BF16 / KVA_F16: 16-bit values, scales NULL;
  *   out_dtype KVA_Q8_0: int8 codes and fp16 scales [n / 32, rows] (one 32-wide block of all
  *     rows contiguous, the layout kva_op_gemm_q8_0 reads), n a multiple of 32: per block of
@@ -164,8 +170,8 @@ int kva_op_add_rmsnorm(const void* x, int32_t x_dtype, int64_t ldx, const void* 
 
 /* Scores of a row of logits: the log softmax at a given token, its normaliser, the entropy
  * and the n_top most probable tokens.
- *   logits      [rows, ld] in dtype (KVA_BF16, KVA_F16 or KVA_F32), n_vocab columns used; any ld
- *               >= n_vocab, pointer aligned to its element
+ *   logits      [rows, ld] in dtype (KVA_BF16, KVA_F16 or KVA_F32), n_vocab columns used (at most
+ *               2^30); any ld >= n_vocab, pointer aligned to its element
  *   tokens      int32 [rows] (device) or NULL.  -1: no token given (logprob 0); any other
  *               value outside 0..n_vocab-1: logprob NaN
  *   logprob     fp32 [rows]: x[token] - lse (with tokens; NULL without)

@@ -77,7 +77,7 @@ def _logp(**kw):
 
 
 @pytest.mark.parametrize("change,want", [
-    (dict(rows=-1), INVALID), (dict(V=0), INVALID), (dict(n_top=-1), INVALID), (dict(n_top=33), TOO_LARGE),
+    (dict(rows=-1), INVALID), (dict(V=0), INVALID), (dict(V=2 ** 30 + 1, ld=2 ** 31), TOO_LARGE), (dict(n_top=-1), INVALID), (dict(n_top=33), TOO_LARGE),
     (dict(dtype=K.KVA_Q8_0), INVALID), (dict(logits=None), INVALID), (dict(ld=99), INVALID),
     (dict(tokens=None), INVALID), (dict(logprob=None), INVALID), (dict(top_id=None), INVALID),
     (dict(top_logprob=None), INVALID), (dict(logits=17), ALIGNMENT), (dict(dtype=K.KVA_F32, logits=18), ALIGNMENT),
