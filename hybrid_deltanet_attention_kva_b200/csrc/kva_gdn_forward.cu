@@ -25,7 +25,9 @@ struct GdnFwd {
   int32_t lens[KVA_GDN_MAX_SEQ];
 };
 
-// runs of at most this many tokens go token by token
+// Sequences of at most this many tokens go token by token, longer ones in runs of 16: at 8 tokens of a
+// 16/48-head layer 5.7 us against 5.1 for one sequence, but 33 against 38 for 16 and 117 against 133
+// for 64; a token more costs 0.5 us, 2.5 us and 11 us, a run nothing until it is full.
 constexpr int kStepTokens = 8;
 
 // two fp32 operations an instruction
@@ -63,7 +65,8 @@ __device__ __forceinline__ float sum8(float v) {  // over the 8 lanes of a row
 // Token by token, for at most kStepTokens tokens.  8 lanes hold a state row in fp32 registers (lane l
 // the columns 32 i + 4 l + j); a block of 256 threads takes 32 RPT rows, RPT a thread, so its k, q, v and
 // gates are read once, together with the state, into shared memory.  HBM bounds it (the state is read
-// and written once).  grid (n_v * D / (32 RPT), n_seq)
+// and written once): one token of 64 sequences, 16/48 heads of 128, 61.5 us, 6.6 TB/s; one of a single
+// sequence 3.0 us, launch and two memory latencies.  grid (n_v * D / (32 RPT), n_seq)
 template <typename T, int D, int RPT>
 __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constant__ GdnFwd p) {
   constexpr int NI = D / 32, ROWS = 32 * RPT, PARTS = D / ROWS, PC = D / 8;
@@ -163,10 +166,25 @@ __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constan
 //     U      = (V^T - S K^T diag(e^gam)) Tm^T              (column s: the update u_s),
 //     O      = S Q^T diag(e^gam) + U M^T,                  M[t,s] = e^(gam_t-gam_s) q_t.k_s (s <= t),
 //     S     <- e^gam_last S + U diag(e^(gam_last-gam)) K.
-// Tm, M and the decays take no state: two preparing warps form them ahead of the chain.  A
-// chain warp owns 16 rows of S as fp32 accumulator fragments, which are also (packed) the A
-// operand of the next product, so a run passes through registers alone: no barrier between the
-// chain's warps, and no trip of S through shared or tensor memory.
+// Tm, M and the decays take no state: preparing warps form them ahead of the chain.  A chain warp
+// owns 16 rows of S as fp32 accumulator fragments, which are also (packed) the A operand of the
+// next product, so a run passes through registers alone: no barrier between the chain's warps, and
+// no trip of S through shared or tensor memory.
+//
+// The state may not see a 16-bit rounding (it carries over thousands of tokens), so S, W, Tm and the
+// updates enter as two 16-bit terms: two products where the partner is K, three where it has two terms
+// itself; the readout's Z takes S's first term, rounded like the output.  That makes 94 MMAs a warp
+// and run (820 cycles of the tensor pipe alone).
+//
+// What bounds it: a run's chain of dependent steps.  16/48 heads of 128, one sequence of 1024
+// tokens (96 blocks, one chain warp a scheduler): 66 us, 1.03 us a run, of which Y and Z 945 cycles, W and U
+// 310, the state's update 390, O and its stores 365; eight sequences 349 us (bf16), where two blocks an SM
+// overlap at 1.8 k cycles a block's run.  Measured and not kept (us for 1 / 8 sequences, before or after
+// other steps): runs of 32 tokens (100 / 399 against 82 / 362), the columns split over pairs of warps (76 /
+// 450 against 68 / 349), the update fused with the next run's Y (75 / 380), 128 rows a block with shared
+// preparation (68 / 324, but 8 % slower for four sequences and short runs), and chunks of 64 tokens on
+// tcgen05 with the state in tensor memory (120 / 372): there every product makes a round trip through
+// tensor memory, 8 conversions a chunk at 0.5-2 k cycles, and an MMA takes about 96 cycles to issue.
 // ============================================================================
 constexpr int CH = 16;          // tokens a run
 constexpr int ROWS = 64;        // state rows a block
@@ -211,12 +229,21 @@ __device__ __forceinline__ uint32_t piece16(int r, int c) {
   return static_cast<uint32_t>(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
 }
 
-// x as two 16-bit terms: hi + lo holds x to the square of the type's half step
+// x as two 16-bit terms, hi + lo.  fp16: hi is x cut to 11 bits, so that the remainder does not wait
+// for a conversion and back (x to 2^-21); bf16: hi is x rounded (x to 2^-16).
 template <typename T>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = F16<T>::pack(x, y);
-  const float2 l = sub2(make_float2(x, y), F16<T>::unpack(hi));
-  lo = F16<T>::pack(l.x, l.y);
+  if constexpr (sizeof(T) == 2 && F16<T>::umma_fmt == 0) {
+    const float2 h = make_float2(__uint_as_float(__float_as_uint(x) & 0xffffe000u),
+                                 __uint_as_float(__float_as_uint(y) & 0xffffe000u));
+    const float2 l = sub2(make_float2(x, y), h);
+    hi = F16<T>::pack(h.x, h.y);
+    lo = F16<T>::pack(l.x, l.y);
+  } else {
+    hi = F16<T>::pack(x, y);
+    const float2 l = sub2(make_float2(x, y), F16<T>::unpack(hi));
+    lo = F16<T>::pack(l.x, l.y);
+  }
 }
 // accumulator fragments of two neighbouring 8-column tiles as an A operand (16 x 16)
 template <typename T>
@@ -613,11 +640,14 @@ template <typename T, int D>
 cudaError_t launch(const GdnFwd& p, int n_seq, int longest, cudaStream_t s) {
   const dim3 grid(p.n_v * (D / ROWS), n_seq);
   if (longest <= kStepTokens) {
-    // two rows a thread where that still leaves four blocks an SM
+    // two rows a thread where that still leaves four blocks an SM (64 sequences, 8 tokens: 117 us against 139
+    // with one row)
     if (static_cast<int64_t>(grid.x) * grid.y >= 4 * num_sms())
       return launch_pdl(gdn_recurrent_kernel<T, D, 2>, grid, dim3(256), 0, s, p);
     return launch_pdl(gdn_recurrent_kernel<T, D, 1>, dim3(p.n_v * (D / 32), n_seq), dim3(256), 0, s, p);
   }
+  // a block that has its SM to itself takes a preparing warp on every scheduler (68 against 82 us for one
+  // sequence of 1024 tokens); two blocks an SM have the registers for two each
   if (static_cast<int64_t>(grid.x) * grid.y <= num_sms()) return launch_chunk<T, D, 4, 1>(p, grid, s);
   return launch_chunk<T, D, 2, 2>(p, grid, s);
 }
@@ -685,7 +715,9 @@ extern "C" int kva_op_gdn_forward(const kva_gdn_forward_args* a, int32_t* err, v
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f16 = a->dtype == KVA_F16;
   const cudaError_t r = a->d == 128
-                            ? (f16 ? launch<__half, 128>(p, a->n_seq, longest, s) : launch<__nv_bfloat16, 128>(p, a->n_seq, longest, s))
-                            : (f16 ? launch<__half, 64>(p, a->n_seq, longest, s) : launch<__nv_bfloat16, 64>(p, a->n_seq, longest, s));
+                            ? (f16 ? launch<__half, 128>(p, a->n_seq, longest, s)
+                                   : launch<__nv_bfloat16, 128>(p, a->n_seq, longest, s))
+                            : (f16 ? launch<__half, 64>(p, a->n_seq, longest, s)
+                                   : launch<__nv_bfloat16, 64>(p, a->n_seq, longest, s));
   return r == cudaSuccess ? KVA_OK : KVA_ERR_CUDA;
 }

@@ -120,7 +120,7 @@ int kva_op_gdn_scan(const void* k, const void* v, const float* gb, float* state,
  *   o_t = scale * S_t q_t
  * v head h reads k and q head h / (n_v / n_k).  The state is held in fp32 throughout.
  * Up to 8 tokens run one after the other in fp32; longer sequences in runs of 16 on the tensor
- * cores, where fp32 operands enter as the sum of two values of `dtype` (an error of 2^-22
+ * cores, where fp32 operands enter as the sum of two values of `dtype` (an error of 2^-21
  * relative with KVA_F16, 2^-16 with KVA_BF16; the state's part of a readout as one value).  With
  * KVA_F16 the state and v - S k must then stay below 65504.  A NaN or an infinity in a token's
  * inputs can reach the tokens of its run before it too. */
