@@ -172,14 +172,16 @@ __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constan
 // no trip of S through shared or tensor memory.
 //
 // The state may not see a 16-bit rounding (it carries over thousands of tokens), so S, W, Tm and the
-// updates enter as two 16-bit terms: two products where the partner is K, three where it has two terms
-// itself; the readout's Z takes S's first term, rounded like the output.  That makes 94 MMAs a warp
-// and run (820 cycles of the tensor pipe alone).
+// updates enter as two fp16 terms: two products where the partner is K, three where it has two terms
+// itself; the readout's Z takes S in one 16-bit term, rounded like the output.  That makes 94 MMAs a warp
+// and run (820 cycles of the tensor pipe alone).  bf16 inputs take fp16 terms as well, in units that
+// follow the data: two bf16 terms left states 3.4e-6 off after 1024 tokens (fp16 terms: 2e-7), three of
+// them would cost 30 % of the time, the units cost 4 to 9 %.
 //
 // What bounds it: a run's chain of dependent steps.  16/48 heads of 128, one sequence of 1024
-// tokens (96 blocks, one chain warp a scheduler): 66 us, 1.03 us a run, of which Y and Z 945 cycles, W and U
-// 310, the state's update 390, O and its stores 365; eight sequences 349 us (bf16), where two blocks an SM
-// overlap at 1.8 k cycles a block's run.  Measured and not kept (us for 1 / 8 sequences, before or after
+// tokens (96 blocks, one chain warp a scheduler): fp16 66 us, 1.03 us a run, of which Y and Z 945 cycles, W
+// and U 310, the state's update 390, O and its stores 365 (bf16 74 us); eight sequences, where two blocks an SM
+// overlap at 1.8 k cycles a block's run (fp16 327 us, bf16 with its units 380 us).  Measured and not kept (us for 1 / 8 sequences, before or after
 // other steps): runs of 32 tokens (100 / 399 against 82 / 362), the columns split over pairs of warps (76 /
 // 450 against 68 / 349), the update fused with the next run's Y (75 / 380), 128 rows a block with shared
 // preparation (68 / 324, but 8 % slower for four sequences and short runs), and chunks of 64 tokens on
@@ -203,7 +205,7 @@ struct Stage {
   static constexpr int ML = MH + CH * CH * 2;
   static constexpr int EG = ML + CH * CH * 2;      // e^gam[16]
   static constexpr int DEC = EG + CH * 4;          // e^(gam_last - gam)[16]
-  static constexpr int GL = DEC + CH * 4;          // e^gam_last
+  static constexpr int GL = DEC + CH * 4;          // e^gam_last, then (bf16) the largest |v|
   static constexpr int BYTES = GL + 128;
 };
 struct Prep {                                      // per preparing warp: L in fp32 (row stride 20), beta
@@ -233,7 +235,7 @@ __device__ __forceinline__ uint32_t piece16(int r, int c) {
 // for a conversion and back (x to 2^-21); bf16: hi is x rounded (x to 2^-16).
 template <typename T>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  if constexpr (sizeof(T) == 2 && F16<T>::umma_fmt == 0) {
+  if constexpr (F16<T>::umma_fmt == 0) {
     const float2 h = make_float2(__uint_as_float(__float_as_uint(x) & 0xffffe000u),
                                  __uint_as_float(__float_as_uint(y) & 0xffffe000u));
     const float2 l = sub2(make_float2(x, y), h);
@@ -244,6 +246,49 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
     const float2 l = sub2(make_float2(x, y), F16<T>::unpack(hi));
     lo = F16<T>::pack(l.x, l.y);
   }
+}
+// bf16 inputs: the chain's products are fp16 as well, in units of a power of two that follows the data.
+// What is at most m is below 2^8 in its units; with keys of norm <= 1 and beta <= 1, W, U and S of a run
+// whose values are at most m and whose state rows have a norm of at most m stay below 18 m: below fp16's
+// 65504, and what fp16 drops is 2^-32 m.
+template <typename T>
+constexpr bool kScaled = F16<T>::umma_fmt == 1;
+struct Scale {
+  float up, down;
+  __device__ __forceinline__ explicit Scale(float m) {
+    const int e = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 7, -100), 100);
+    up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  }
+};
+constexpr float kNoScale = 1e30f;  // NaN and what is from here on set no scale (their rows are lost, the others not)
+// the warp's largest |x|
+template <int N>
+__device__ __forceinline__ float warp_largest(const float (&x)[N][4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(x[i][j]));
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  if (m < kNoScale) return m;
+  m = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(x[i][j]) < kNoScale ? fabsf(x[i][j]) : 0.f);
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
+template <int N>
+__device__ __forceinline__ void scale_all(float (&x)[N][4], float f) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const float2 y = mul2(make_float2(x[i][j], x[i][j + 1]), make_float2(f, f));
+      x[i][j] = y.x;
+      x[i][j + 1] = y.y;
+    }
 }
 // accumulator fragments of two neighbouring 8-column tiles as an A operand (16 x 16)
 template <typename T>
@@ -453,9 +498,43 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          split2<T>(x[8 * i + 2 * j] * bb[8 * i + 2 * j], x[8 * i + 2 * j + 1] * bb[8 * i + 2 * j + 1], hi[j], lo[j]);
+          split2<__half>(x[8 * i + 2 * j] * bb[8 * i + 2 * j], x[8 * i + 2 * j + 1] * bb[8 * i + 2 * j + 1], hi[j], lo[j]);
         *reinterpret_cast<uint4*>(st + St::TH + piece16(lane, i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(st + St::TL + piece16(lane, i)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+    if constexpr (kScaled<T>) {
+      // the largest |v| (as bf16 pairs; NaN falls out, and with a value near infinity it is looked up again)
+      __nv_bfloat162 pair = __float2bfloat162_rn(0.f);
+#pragma unroll
+      for (int i = 0; i < CH * ROWS / 256; ++i) {
+        const uint4 x = reinterpret_cast<const uint4*>(st + St::V)[32 * i + lane];
+        const __nv_bfloat162* v2 = reinterpret_cast<const __nv_bfloat162*>(&x);
+        pair = __hmax2(pair, __hmax2(__hmax2(__habs2(v2[0]), __habs2(v2[1])), __hmax2(__habs2(v2[2]), __habs2(v2[3]))));
+      }
+      float big = fmaxf(__low2float(pair), __high2float(pair));
+      big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+      if (big >= kNoScale) {
+        big = 0.f;
+        for (int i = lane; i < CH * ROWS; i += 32) {
+          const float f = fabsf(F16<T>::to(reinterpret_cast<const T*>(st + St::V)[i]));
+          if (f < kNoScale) big = fmaxf(big, f);
+        }
+        big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+      }
+      if (lane == 0) *reinterpret_cast<float*>(st + St::GL + 4) = big;
+      // the chain's products take K in fp16: exact but for what is below 2^-17
+#pragma unroll 2
+      for (int i = lane; i < CH * D / 8; i += 32) {
+        uint4* k8 = reinterpret_cast<uint4*>(st + St::K) + i;
+        uint4 x = *k8;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = F16<T>::unpack(w[j]);
+          w[j] = pack_f16(f.x, f.y);
+        }
+        *k8 = x;
       }
     }
     __syncwarp();
@@ -485,6 +564,15 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
     S[j][3] = c.y;
   }
   T* out = static_cast<T*>(p.out) + seq * p.out_seq + h * D + half * ROWS + warp * 16 + 2 * cq;
+  // bf16: S is held in units of `sc.up`; `norm` bounds the norm of its rows
+  const float root = D == 128 ? 11.32f : 8.f;  // sqrt(D): a row's norm is at most that times its largest entry
+  float norm = 0.f;
+  Scale sc(1.f);
+  if constexpr (kScaled<T>) {
+    norm = root * warp_largest(S);
+    sc = Scale(norm);
+    scale_all(S, sc.down);
+  }
 
   for (int c = 0; c < n_runs; ++c) {
     if (!mbar_wait(&full[c % NST], (c / NST) & 1, abort_flag)) {
@@ -506,40 +594,58 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
         ldmatrix_x4(qf[(ks + 1) & 1], sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + 2 + (mi >> 1)));
       }
       uint32_t ah[4], al[4];
-      split_a<T>(S[2 * ks], S[2 * ks + 1], ah, al);
-      mma2<T>(y[0], y[1], ah, kf[ks & 1], 0, 2, 1, 3);
-      mma2<T>(yl[0], yl[1], al, kf[ks & 1], 0, 2, 1, 3);
-      mma2<T>(z[0], z[1], ah, qf[ks & 1], 0, 2, 1, 3);
+      split_a<__half>(S[2 * ks], S[2 * ks + 1], ah, al);
+      mma2<__half>(y[0], y[1], ah, kf[ks & 1], 0, 2, 1, 3);
+      mma2<__half>(yl[0], yl[1], al, kf[ks & 1], 0, 2, 1, 3);
+      if constexpr (kScaled<T>) {  // (q may be anything: it stays bf16)
+        const float(&s0)[4] = S[2 * ks], (&s1)[4] = S[2 * ks + 1];
+        const uint32_t az[4] = {F16<T>::pack(s0[0], s0[1]), F16<T>::pack(s0[2], s0[3]), F16<T>::pack(s1[0], s1[1]),
+                                F16<T>::pack(s1[2], s1[3])};
+        mma2<T>(z[0], z[1], az, qf[ks & 1], 0, 2, 1, 3);
+      } else {
+        mma2<T>(z[0], z[1], ah, qf[ks & 1], 0, 2, 1, 3);
+      }
     }
     // W = V^T - Y diag(e^gam)
     uint32_t vf[4], wh[4], wl[4];
     ldmatrix_x4_trans(vf, sst + St::V + piece<2 * ROWS>((mi >> 1) * 8 + lr, 2 * warp + (mi & 1)));
-    {
-      float w[2][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 e = *reinterpret_cast<const float2*>(st + St::EG + (8 * i + 2 * cq) * 4);
-        const float2 v0 = F16<T>::unpack(vf[2 * i]), v1 = F16<T>::unpack(vf[2 * i + 1]);
-        w[i][0] = v0.x - e.x * (y[i][0] + yl[i][0]);
-        w[i][1] = v0.y - e.y * (y[i][1] + yl[i][1]);
-        w[i][2] = v1.x - e.x * (y[i][2] + yl[i][2]);
-        w[i][3] = v1.y - e.y * (y[i][3] + yl[i][3]);
-        z[i][0] *= e.x;
-        z[i][1] *= e.y;
-        z[i][2] *= e.x;
-        z[i][3] *= e.y;
-      }
-      split_a<T>(w[0], w[1], wh, wl);
+    const float2 gv = *reinterpret_cast<const float2*>(st + St::GL);
+    float decay = gv.x, up = 1.f;  // of S into the next run; the units of Y and Z
+    if constexpr (kScaled<T>) {
+      // the run's units, from its values and the state's decayed rows
+      up = sc.up;
+      const Scale now(fmaxf(gv.y, gv.x * norm));
+      decay *= sc.up * now.down;
+      sc = now;
+      // S <- e^g S (I - beta k k^T) + beta v k^T, 16 times
+      norm = fmaf(16.f, gv.y, gv.x * norm);
     }
+    float w[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float2 e = *reinterpret_cast<const float2*>(st + St::EG + (8 * i + 2 * cq) * 4);
+      if constexpr (kScaled<T>) e = mul2(e, make_float2(up, up));
+      const float2 v0 = F16<T>::unpack(vf[2 * i]), v1 = F16<T>::unpack(vf[2 * i + 1]);
+      w[i][0] = v0.x - e.x * (y[i][0] + yl[i][0]);
+      w[i][1] = v0.y - e.y * (y[i][1] + yl[i][1]);
+      w[i][2] = v1.x - e.x * (y[i][2] + yl[i][2]);
+      w[i][3] = v1.y - e.y * (y[i][3] + yl[i][3]);
+      z[i][0] *= e.x;
+      z[i][1] *= e.y;
+      z[i][2] *= e.x;
+      z[i][3] *= e.y;
+    }
+    if constexpr (kScaled<T>) scale_all(w, sc.down);
+    split_a<__half>(w[0], w[1], wh, wl);
     // U = W Tm^T
     float u[2][4] = {}, ul[2][4] = {};
     {
       uint32_t th[4], tl[4];
       ldmatrix_x4(th, sst + St::TH + piece16((mi & 1) * 8 + lr, mi >> 1));
       ldmatrix_x4(tl, sst + St::TL + piece16((mi & 1) * 8 + lr, mi >> 1));
-      mma2<T>(u[0], u[1], wh, th, 0, 2, 1, 3);
-      mma2<T>(ul[0], ul[1], wl, th, 0, 2, 1, 3);
-      mma2<T>(ul[0], ul[1], wh, tl, 0, 2, 1, 3);
+      mma2<__half>(u[0], u[1], wh, th, 0, 2, 1, 3);
+      mma2<__half>(ul[0], ul[1], wl, th, 0, 2, 1, 3);
+      mma2<__half>(ul[0], ul[1], wh, tl, 0, 2, 1, 3);
     }
     uint32_t uh[4], uo[4], dh[4], dl[4];
     {
@@ -554,26 +660,20 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
         dd[i][2] = u[i][2] * e.x;
         dd[i][3] = u[i][3] * e.y;
       }
+      split_a<__half>(dd[0], dd[1], dh, dl);
+      if constexpr (kScaled<T>) scale_all(u, sc.up);
       split_a<T>(u[0], u[1], uh, uo);
-      split_a<T>(dd[0], dd[1], dh, dl);
     }
     // S <- e^gam_last S + U diag(dec) K
-    const float gl = *reinterpret_cast<const float*>(st + St::GL);
-#pragma unroll
-    for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const float2 x = mul2(make_float2(S[j][e], S[j][e + 1]), make_float2(gl, gl));
-        S[j][e] = x.x;
-        S[j][e + 1] = x.y;
-      }
+    scale_all(S, decay);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint32_t kt[4];
       ldmatrix_x4_trans(kt, sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
-      mma2<T>(S[2 * ks], S[2 * ks + 1], dh, kt, 0, 1, 2, 3);
-      mma2<T>(S[2 * ks], S[2 * ks + 1], dl, kt, 0, 1, 2, 3);
+      mma2<__half>(S[2 * ks], S[2 * ks + 1], dh, kt, 0, 1, 2, 3);
+      mma2<__half>(S[2 * ks], S[2 * ks + 1], dl, kt, 0, 1, 2, 3);
     }
+    if (kScaled<T> && (c & 7) == 7) norm = fminf(norm, root * sc.up * warp_largest(S));
     // O = Z diag(e^gam) + U M^T, written token-major
     {
       uint32_t mh[4], ml[4];
@@ -596,6 +696,7 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
       }
     }
   }
+  if constexpr (kScaled<T>) scale_all(S, sc.up);
 #pragma unroll
   for (int j = 0; j < D / 8; ++j) {
     *reinterpret_cast<float2*>(p.state_out + srow + 8 * j) = make_float2(S[j][0], S[j][1]);
