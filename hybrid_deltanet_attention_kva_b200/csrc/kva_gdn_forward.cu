@@ -180,21 +180,20 @@ __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constan
 //
 // What bounds it: a run's chain of dependent steps.  16/48 heads of 128, one sequence of 1024
 // tokens (96 blocks, one chain warp a scheduler): fp16 66 us, 1.03 us a run, of which Y and Z 945 cycles, W
-// and U 310, the state's update 390, O and its stores 365 (bf16 74 us); eight sequences, where two blocks an SM
-// overlap at 1.8 k cycles a block's run (fp16 327 us, bf16 with its units 380 us).  Measured and not kept (us for 1 / 8 sequences, before or after
-// other steps): runs of 32 tokens (100 / 399 against 82 / 362), the columns split over pairs of warps (76 /
-// 450 against 68 / 349), the update fused with the next run's Y (75 / 380), 128 rows a block with shared
-// preparation (68 / 324, but 8 % slower for four sequences and short runs), and chunks of 64 tokens on
-// tcgen05 with the state in tensor memory (120 / 372): there every product makes a round trip through
-// tensor memory, 8 conversions a chunk at 0.5-2 k cycles, and an MMA takes about 96 cycles to issue.
+// and U 310, the state's update 390, O and its stores 365 (bf16 74 us); eight sequences, where two chain
+// warps share a scheduler: fp16 301 us, bf16 with its units 357 us.  Measured and not kept (us for 1 / 8
+// sequences, against the state of that step): runs of 32 tokens (100 / 399 against 82 / 362), the columns
+// split over pairs of warps (76 / 450 against 68 / 349), the update fused with the next run's Y (75 / 380
+// against 68 / 349), readouts by warps of their own (69 / 363 against 66 / 349), and chunks of 64 tokens on
+// tcgen05 with the state in tensor memory (120 / 372 against 82 / 362): there every product makes a round
+// trip through tensor memory, 8 conversions a chunk at 0.5-2 k cycles, and an MMA takes about 96 cycles to
+// issue.
 // ============================================================================
 constexpr int CH = 16;          // tokens a run
-constexpr int ROWS = 64;        // state rows a block
-constexpr int CHAIN = ROWS / 16;  // chain warps
 constexpr int LOADED = 4;       // runs in flight behind those being prepared
 constexpr int NST = 8;          // stages: the run of AHEAD + 1 own steps back is consumed when its place is needed
 
-template <int D>
+template <int D, int ROWS>       // ROWS state rows a block
 struct Stage {
   static constexpr int K = 0;                      // [16][D], 16-byte pieces xor-swizzled by row
   static constexpr int Q = K + CH * D * 2;
@@ -212,9 +211,9 @@ struct Prep {                                      // per preparing warp: L in f
   static constexpr int LDL = 20;
   static constexpr int BYTES = (CH * LDL + CH) * 4;
 };
-template <int D, int PREP>
+template <int D, int ROWS, int PREP>
 struct Chunk {
-  static constexpr int L = NST * Stage<D>::BYTES;
+  static constexpr int L = NST * Stage<D, ROWS>::BYTES;
   static constexpr int BAR = L + PREP * Prep::BYTES;  // full[NST], empty[NST]
   static constexpr int MISC = BAR + 2 * NST * 8;      // abort flag
   static constexpr int BYTES = MISC + 16;
@@ -318,12 +317,12 @@ __device__ __forceinline__ void mma2(float (&d0)[4], float (&d1)[4], const uint3
 }
 
 // A preparing warp: runs pw, pw + PREP, ...
-template <typename T, int D, int PREP>
+template <typename T, int D, int ROWS, int PREP>
 __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int seq, int len, int pw, int lane,
                              volatile int* abort_flag) {
-  using St = Stage<D>;
+  using St = Stage<D, ROWS>;
   constexpr int AHEAD = LOADED / PREP;  // own runs in flight behind the one worked on
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Chunk<D, PREP>::BAR);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Chunk<D, ROWS, PREP>::BAR);
   uint64_t* empty = full + NST;
   const int kh = h / (p.n_v / p.n_k), n_runs = (len + CH - 1) / CH;
   const T* q = static_cast<const T*>(p.q) + seq * p.q_seq + kh * D;
@@ -331,7 +330,7 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
   const T* v = static_cast<const T*>(p.v) + seq * p.v_seq + h * D + half * ROWS;
   const float* g = p.gb + (static_cast<int64_t>(seq) * 2 * p.n_v + h) * p.T;
   const float* b = g + static_cast<int64_t>(p.n_v) * p.T;
-  float* Ls = reinterpret_cast<float*>(sm + Chunk<D, PREP>::L + pw * Prep::BYTES);
+  float* Ls = reinterpret_cast<float*>(sm + Chunk<D, ROWS, PREP>::L + pw * Prep::BYTES);
   const uint32_t base = smem_u32(sm);
 
   // a lane copies one 16-byte column of every RK-th (V: RV-th) row of a run
@@ -543,11 +542,11 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
   cp_async_wait<0>();
 }
 
-template <typename T, int D, int PREP>
+template <typename T, int D, int ROWS, int PREP>
 __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int seq, int len, int warp, int lane,
                            volatile int* abort_flag) {
-  using St = Stage<D>;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Chunk<D, PREP>::BAR);
+  using St = Stage<D, ROWS>;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Chunk<D, ROWS, PREP>::BAR);
   uint64_t* empty = full + NST;
   const int n_runs = (len + CH - 1) / CH;
   const int mi = lane >> 3, lr = lane & 7, gr = lane >> 2, cq = lane & 3;
@@ -704,14 +703,14 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
   }
 }
 
-// grid (n_v * D / 64, n_seq): 64 state rows of one head, four chain warps and PREP preparing ones
-template <typename T, int D, int PREP, int BLOCKS>
-__global__ void __launch_bounds__(32 * (CHAIN + PREP), BLOCKS) gdn_chunk_kernel(const __grid_constant__ GdnFwd p) {
+// grid (n_v * D / ROWS, n_seq): ROWS state rows of one head, a chain warp for every 16 and PREP preparing ones
+template <typename T, int D, int ROWS, int PREP, int BLOCKS>
+__global__ void __launch_bounds__(32 * (ROWS / 16 + PREP), BLOCKS) gdn_chunk_kernel(const __grid_constant__ GdnFwd p) {
   extern __shared__ __align__(128) uint8_t sm[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Chunk<D, PREP>::BAR);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Chunk<D, PREP>::MISC);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Chunk<D, ROWS, PREP>::BAR);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Chunk<D, ROWS, PREP>::MISC);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int HALVES = D / ROWS;
+  constexpr int HALVES = D / ROWS, CHAIN = ROWS / 16;
   const int h = blockIdx.x / HALVES, half = blockIdx.x % HALVES, seq = blockIdx.y;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
@@ -724,33 +723,40 @@ __global__ void __launch_bounds__(32 * (CHAIN + PREP), BLOCKS) gdn_chunk_kernel(
   __syncthreads();
   griddep_wait_and_release();
   const int len = p.has_lens ? p.lens[seq] : p.T;
-  if (warp < CHAIN) chain_runs<T, D, PREP>(p, sm, h, half, seq, len, warp, lane, abort_flag);
-  else prepare_runs<T, D, PREP>(p, sm, h, half, seq, len, warp - CHAIN, lane, abort_flag);
+  if (warp < CHAIN) chain_runs<T, D, ROWS, PREP>(p, sm, h, half, seq, len, warp, lane, abort_flag);
+  else prepare_runs<T, D, ROWS, PREP>(p, sm, h, half, seq, len, warp - CHAIN, lane, abort_flag);
 }
 
-template <typename T, int D, int PREP, int BLOCKS>
-cudaError_t launch_chunk(const GdnFwd& p, dim3 grid, cudaStream_t s) {
-  auto kern = gdn_chunk_kernel<T, D, PREP, BLOCKS>;
-  constexpr int bytes = Chunk<D, PREP>::BYTES;
+template <typename T, int D, int ROWS, int PREP, int BLOCKS>
+cudaError_t launch_chunk(const GdnFwd& p, int n_seq, cudaStream_t s) {
+  auto kern = gdn_chunk_kernel<T, D, ROWS, PREP, BLOCKS>;
+  constexpr int bytes = Chunk<D, ROWS, PREP>::BYTES;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, grid, dim3(32 * (CHAIN + PREP)), bytes, s, p);
+  return launch_pdl(kern, dim3(p.n_v * (D / ROWS), n_seq), dim3(32 * (ROWS / 16 + PREP)), bytes, s, p);
 }
 
 template <typename T, int D>
 cudaError_t launch(const GdnFwd& p, int n_seq, int longest, cudaStream_t s) {
-  const dim3 grid(p.n_v * (D / ROWS), n_seq);
+  const int sms = num_sms();
+  const int64_t blocks = static_cast<int64_t>(p.n_v) * (D / 64) * n_seq;  // of 64 state rows
   if (longest <= kStepTokens) {
     // two rows a thread where that still leaves four blocks an SM (64 sequences, 8 tokens: 117 us against 139
     // with one row)
-    if (static_cast<int64_t>(grid.x) * grid.y >= 4 * num_sms())
-      return launch_pdl(gdn_recurrent_kernel<T, D, 2>, grid, dim3(256), 0, s, p);
+    if (blocks >= 4 * sms)
+      return launch_pdl(gdn_recurrent_kernel<T, D, 2>, dim3(p.n_v * (D / 64), n_seq), dim3(256), 0, s, p);
     return launch_pdl(gdn_recurrent_kernel<T, D, 1>, dim3(p.n_v * (D / 32), n_seq), dim3(256), 0, s, p);
   }
-  // a block that has its SM to itself takes a preparing warp on every scheduler (68 against 82 us for one
-  // sequence of 1024 tokens); two blocks an SM have the registers for two each
-  if (static_cast<int64_t>(grid.x) * grid.y <= num_sms()) return launch_chunk<T, D, 4, 1>(p, grid, s);
-  return launch_chunk<T, D, 2, 2>(p, grid, s);
+  // A block that has its SM to itself takes a preparing warp on every scheduler (68 against 82 us for one
+  // sequence of 1024 tokens).  With more work a head's 128 rows share one preparation, 6 to 9 % faster (8
+  // sequences, bf16: 358 against 381 us) but for a last round that fills less than half of the SMs: there two
+  // blocks of 64 rows an SM end sooner (4 sequences: 220 against 239 us).
+  if (blocks <= sms) return launch_chunk<T, D, 64, 4, 1>(p, n_seq, s);
+  if constexpr (D == 128) {
+    const int64_t last = blocks / 2 % sms;
+    if (last == 0 || 2 * last >= sms) return launch_chunk<T, D, 128, 4, 1>(p, n_seq, s);
+  }
+  return launch_chunk<T, D, 64, 2, 2>(p, n_seq, s);
 }
 
 bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
