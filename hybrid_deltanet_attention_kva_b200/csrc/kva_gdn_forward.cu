@@ -197,7 +197,7 @@ template <int D, int ROWS>       // ROWS state rows a block
 struct Stage {
   static constexpr int K = 0;                      // [16][D], 16-byte pieces xor-swizzled by row
   static constexpr int Q = K + CH * D * 2;
-  static constexpr int V = Q + CH * D * 2;         // [16][64], this block's columns
+  static constexpr int V = Q + CH * D * 2;         // [16][ROWS], this block's columns
   static constexpr int TH = V + CH * ROWS * 2;     // Tm as two 16-bit terms, [s][t]
   static constexpr int TL = TH + CH * CH * 2;
   static constexpr int MH = TL + CH * CH * 2;      // M as two 16-bit terms, [t][s]
@@ -569,7 +569,7 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
   Scale sc(1.f);
   if constexpr (kScaled<T>) {
     norm = root * warp_largest(S);
-    sc = Scale(norm);
+    sc = Scale(n_runs ? norm : 128.f);  // (units of 1 without tokens: the state goes out as it came)
     scale_all(S, sc.down);
   }
 

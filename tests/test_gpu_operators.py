@@ -251,6 +251,34 @@ def test_gdn_scales_that_change_and_lost_columns(K, T, dt):
     assert ((S2 - S3)[0].cpu()[~spoiled].abs() <= lim).all()
 
 
+@pytest.mark.parametrize("T", [5, 40])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+def test_gdn_a_sequence_without_tokens_keeps_any_state(K, T, dt):
+    """Next to sequences with tokens, bit for bit: values 10^68 apart, subnormals and infinities."""
+    q, k, v, gb, S = make_gdn(2, T, 2, 4, 128, dt, seed=9)
+    S[0] = torch.exp2(252 * torch.rand(S[0].shape, generator=torch.Generator().manual_seed(3)) - 126).cuda()
+    S[0, :, ::7] = 2.0 ** -140
+    S[0, 1, 3, 5], S[0, 2, 3, 5], S[0, 3, ::2] = math.inf, -3e38, 0.0
+    out, S1 = run_gdn(K, q, k, v, gb, S, lens=[0, T])
+    assert torch.equal(S1[0], S[0])
+    check_gdn(out[1:], S1[1:], q[1:], k[1:], v[1:], gb[1:], S[1:], [T])
+
+
+@pytest.mark.parametrize("n,nv", [(1, 70), (1, 100), (3, 50), (5, 47)])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+def test_gdn_more_heads_than_the_gpu_takes_at_once(K, n, nv, dt):
+    """Up to and past the counts of heads at which the work is laid out in another way, with ragged
+    lengths, in place."""
+    T = 36
+    lens = [T - 3 * i for i in range(n)]
+    q, k, v, gb, S = make_gdn(n, T, 1, nv, 128, dt, seed=10)
+    out, S1 = run_gdn(K, q, k, v, gb, S, lens=lens)
+    check_gdn(out, S1, q, k, v, gb, S, lens)
+    S2, out2 = S.clone(), torch.full_like(out, NAN)
+    K.kva_op_gdn_forward(q, k, v, gb, S2, S2, out2, lens=lens)
+    assert torch.equal(S2, S1) and torch.equal(out2.nan_to_num(), out.nan_to_num())
+
+
 def test_gdn_scan_and_forward_reach_one_state(K):
     """The state of kva_op_gdn_scan (16-bit operands, its own 1e-2) and of this operator."""
     T, nk, nv, d = 130, 2, 6, 128
