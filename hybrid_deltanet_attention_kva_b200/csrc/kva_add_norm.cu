@@ -46,13 +46,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
-// One q8_0 code, round(r) half away from zero for |r| < 128, without the conversion unit (a quarter
-// of the other units' rate): |r| + 0.5 + 2^22 cut to steps of 0.5 holds floor(|r| + 0.5) above its
-// last mantissa bit.
-__device__ __forceinline__ uint32_t q8_code(float r) {
-  const uint32_t c = (__float_as_uint(__fadd_rz(fabsf(r), 4194304.5f)) >> 1) & 0x7fu;
-  const uint32_t s = static_cast<uint32_t>(__float_as_int(r) >> 31);
-  return (c ^ s) - s;
+// One q8_0 code in the low byte, y inv to the nearest integer, in one instruction and without the
+// conversion unit: in the sum with 1.5 x 2^23 a last place is 1, and its low byte is the code in two's
+// complement.
+__device__ __forceinline__ uint32_t q8_code(float y, float inv) {
+  return __float_as_uint(fmaf(y, inv, 12582912.f));
 }
 __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {  // low bytes
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
@@ -122,11 +120,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
       if (i < n) {
         const bool fine = amax < __int_as_float(0x7f800000);
         const float d = amax * (1.f / 127.f);
-        // 127 / max off by 2 ulp moves a code only where y / d is that near to a half.  (From a
-        // subnormal d the reciprocal could overflow; such a d is 0 in fp16, whatever the codes.)
-        const float inv = fine && d >= 1.1754944e-38f ? __fdividef(127.f, amax) : 0.f;
+        // 127 / max, larger by 2^-21: more than the quotient's 2 ulp, so that a half goes away from zero;
+        // what is nearer to a half than 127 x 2^-20 may too.  (From a subnormal d the reciprocal could
+        // overflow; such a d is 0 in fp16, whatever the codes.)
+        const float inv = fine && d >= 1.1754944e-38f ? __fdividef(127.00006f, amax) : 0.f;
         uint32_t c = 0;
-        if (fine) c = pack4(q8_code(y.x * inv), q8_code(y.y * inv), q8_code(y.z * inv), q8_code(y.w * inv));
+        if (fine) c = pack4(q8_code(y.x, inv), q8_code(y.y, inv), q8_code(y.z, inv), q8_code(y.w, inv));
         *reinterpret_cast<uint32_t*>(out + i) = c;
         if ((threadIdx.x & 7) == 0)
           scales[static_cast<int64_t>(i >> 5) * rows + row] = __float2half_rn(fine ? d : __int_as_float(0x7fffffff));
