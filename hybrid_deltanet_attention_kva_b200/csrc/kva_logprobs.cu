@@ -7,7 +7,7 @@
 // look at a few threads' pieces only: the n_top-th largest of 64 thread groups' maxima is a lower bound
 // of the n_top-th largest logit, and about n_top (1 + n_top / 128) logits reach it.  (A warp's sorted list, updated on the way, would issue more than the sums do.)
 //
-// 1024 rows of 131072 bf16 logits, 8 alternatives: 53.4 us, 5.0 TB/s.  A logit takes about 8
+// 1024 rows of 131072 bf16 logits, 8 alternatives: 52.7 us, 5.1 TB/s.  A logit takes about 8
 // instructions (conversion, half a maximum, half a multiply-add, clamp, exponential, half a sum and half a
 // multiply-add), so the issue slots are busy too, and a row's joining and second look (10 k of 40 k
 // cycles of its block) are hidden only by the SM's two other blocks.  One row in a cluster of 8: 5.5 us,
@@ -485,8 +485,14 @@ cudaError_t launch(const LpArgs& p, int rows, cudaStream_t s) {
 }
 template <typename T>
 cudaError_t launch(const LpArgs& p, int rows, cudaStream_t s) {
-  // short rows take small blocks, so that a thread still has a batch of pieces
-  return (p.V + Piece<T>::N - 1) / Piece<T>::N <= 1024 ? launch<T, 128>(p, rows, s) : launch<T, 512>(p, rows, s);
+  // Short rows take small blocks, so that a thread still has a batch of pieces.  So do many rows, where more
+  // blocks an SM hide each other's joins and a thread has more pieces for its share of one: with 256 threads
+  // against 512, 8192 x 32000 bf16 118 against 145 us, 8192 x 65536 195 against 222; but 512 x 32000 15.3
+  // against 13.5, 1024 x 65536 34.1 against 32.5 (the last round of blocks), 4096 x 131072 192 against 190.
+  const int np = (p.V + Piece<T>::N - 1) / Piece<T>::N, sms = num_sms();
+  if (np <= 1024) return launch<T, 128>(p, rows, s);
+  if (rows >= 6 * sms && np <= (rows >= 12 * sms ? 8192 : 4096)) return launch<T, 256>(p, rows, s);
+  return launch<T, 512>(p, rows, s);
 }
 
 }  // namespace

@@ -430,6 +430,13 @@ def test_token_logprobs(K, rows, V, dt, n_top):
     check_logp(K, x, min(n_top, V))
 
 
+@pytest.mark.parametrize("rows,V,dt", [(1000, 9001, torch.bfloat16), (1000, 16390, torch.float32),
+                                       (1900, 6000, torch.float32), (1900, 8195, torch.float16)])
+def test_token_logprobs_many_rows(K, rows, V, dt):
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    check_logp(K, (3 * torch.randn(rows, V, generator=gen, device="cuda")).to(dt), 8)
+
+
 @pytest.mark.parametrize("dt", [torch.float32, torch.float16, torch.bfloat16])
 def test_token_logprobs_any_alignment(K, dt):
     """Rows that begin at every offset inside a 16-byte piece."""
