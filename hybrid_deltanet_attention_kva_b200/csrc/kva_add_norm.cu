@@ -59,11 +59,11 @@ __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, ui
 // TPR threads (a warp, or the block) take a row: NV groups of 4 values each, held in registers
 // from the one read of x and h to the last write.  NV is the next of 4, 6 and 8 (fewer registers, more
 // rows in flight).  HBM bounds the 16-bit forms: 8192 x 5120 bf16 50.5 us (6.6 TB/s, the measured copy rate);
-// the q8_0 form also the conversion: 1024 x 5120 fp32 14.8 us (4.6 TB/s; 13.0 with a 16-bit output), 8192 x
-// 5120 bf16 55.6 us (5.3 TB/s); the scattered scales cost nothing measurable.  One row 2.0 us.  Measured and
+// the q8_0 form also the conversion: 1024 x 5120 fp32 14.9 us (4.6 TB/s; 13.0 with a 16-bit output), 8192 x
+// 5120 bf16 56.2 us (5.3 TB/s); the scattered scales cost nothing measurable.  One row 2.0 us.  Measured and
 // not kept for q8_0: five or six blocks an SM (spills, 1.3 and 1.5 x the time); blocks as wide as a row needs
 // with 8 values a thread (the same for fp32, 8192 x 5120 bf16 77 against 61 us); 8 values in a row a thread
-// (14.5 against 14.8 us, bf16 68 against 56).
+// (14.5 against 14.8 us, bf16 68 against 56 us).
 template <typename TX, typename TH, typename TO, int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     add_rmsnorm_kernel(const TX* __restrict__ x, int64_t ldx, const TH* h, TH* h_out, int64_t ldh,
@@ -123,10 +123,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
       if (i < n) {
         const bool fine = amax < __int_as_float(0x7f800000);
         const float d = amax * (1.f / 127.f);
-        // 127 / max, larger by 2^-21: more than the quotient's 2 ulp, so that a half goes away from zero;
-        // what is nearer to a half than 127 x 2^-20 may too.  (From a subnormal d the reciprocal could
-        // overflow; such a d is 0 in fp16, whatever the codes.)
-        const float inv = fine && d >= 1.1754944e-38f ? __fdividef(127.00006f, amax) : 0.f;
+        // 127 / max to the last place, and one up, so that a half goes away from zero; what is nearer to a
+        // half than 127 x 2^-22 may too.  (From a subnormal d the reciprocal could overflow; such a d is 0 in
+        // fp16, whatever the codes.)
+        const float r = __fdividef(1.f, amax), near = 127.f * r;
+        const float up = __uint_as_float(__float_as_uint(fmaf(fmaf(-amax, near, 127.f), r, near)) + 1);
+        const float inv = fine && d >= 1.1754944e-38f ? up : 0.f;
         uint32_t c = 0;
         if (fine) c = pack4(q8_code(y.x, inv), q8_code(y.y, inv), q8_code(y.z, inv), q8_code(y.w, inv));
         *reinterpret_cast<uint32_t*>(out + i) = c;
