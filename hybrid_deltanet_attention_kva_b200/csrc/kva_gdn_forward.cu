@@ -3,6 +3,8 @@
 //     S_t = e^(g_t) S_(t-1) + u_t k_t^T,   o_t = scale S_t q_t.
 // Row v of S takes only v_t[v], k_t and the gates, so the d rows of a head are
 // independent; the tokens are sequential.
+#include <algorithm>
+
 #include "../../include/kva_ops.h"
 #include "kva_common.cuh"
 
@@ -23,7 +25,9 @@ struct GdnFwd {
   float scale;
   int* err;
   int32_t lens[KVA_GDN_MAX_SEQ];
+  uint8_t order[KVA_GDN_MAX_SEQ];  // with lens, in runs: the sequences, longest first
 };
+static_assert(KVA_GDN_MAX_SEQ <= 256, "a sequence's number takes a byte");
 
 // Sequences of at most this many tokens go token by token, longer ones in runs of 16: at 8 tokens of a
 // 16/48-head layer 5.7 us against 5.1 for one sequence, but 33 against 38 for 16 and 117 against 133
@@ -711,7 +715,7 @@ __global__ void __launch_bounds__(32 * (ROWS / 16 + PREP), BLOCKS) gdn_chunk_ker
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Chunk<D, ROWS, PREP>::MISC);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int HALVES = D / ROWS, CHAIN = ROWS / 16;
-  const int h = blockIdx.x / HALVES, half = blockIdx.x % HALVES, seq = blockIdx.y;
+  const int h = blockIdx.x / HALVES, half = blockIdx.x % HALVES;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&bars[i], 1);
@@ -722,6 +726,7 @@ __global__ void __launch_bounds__(32 * (ROWS / 16 + PREP), BLOCKS) gdn_chunk_ker
   }
   __syncthreads();
   griddep_wait_and_release();
+  const int seq = p.has_lens ? p.order[blockIdx.y] : blockIdx.y;
   const int len = p.has_lens ? p.lens[seq] : p.T;
   if (warp < CHAIN) chain_runs<T, D, ROWS, PREP>(p, sm, h, half, seq, len, warp, lane, abort_flag);
   else prepare_runs<T, D, ROWS, PREP>(p, sm, h, half, seq, len, warp - CHAIN, lane, abort_flag);
@@ -797,6 +802,13 @@ extern "C" int kva_op_gdn_forward(const kva_gdn_forward_args* a, int32_t* err, v
       if (a->lens[i] < 0 || a->lens[i] > a->T) return KVA_ERR_INVALID_ARG;
       p.lens[i] = a->lens[i];
       if (a->lens[i] > longest) longest = a->lens[i];
+    }
+    // the blocks of long sequences start first, so that the last ones to start are short (bf16, 16/48 heads:
+    // 8 sequences of 1 to 1024 tokens 206 to 161 us, 16 of them 276 to 258, 32 of 1 to 512 409 to 379; 128 of 1
+    // to 64 411 to 419)
+    if (longest > kStepTokens) {
+      for (int i = 0; i < a->n_seq; ++i) p.order[i] = static_cast<uint8_t>(i);
+      std::stable_sort(p.order, p.order + a->n_seq, [&](int x, int y) { return p.lens[x] > p.lens[y]; });
     }
   }
   p.q = a->q;

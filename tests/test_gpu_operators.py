@@ -279,6 +279,16 @@ def test_gdn_more_heads_than_the_gpu_takes_at_once(K, n, nv, dt):
     assert torch.equal(S2, S1) and torch.equal(out2.nan_to_num(), out.nan_to_num())
 
 
+def test_gdn_as_many_sequences_as_a_call_takes(K):
+    n = K.kva.GDN_MAX_SEQ
+    lens = [(7 * i) % 20 for i in range(n)]
+    q, k, v, gb, S = make_gdn(n, 19, 1, 2, 64, torch.bfloat16, seed=11)
+    out, S1 = run_gdn(K, q, k, v, gb, S, lens=lens)
+    check_gdn(out, S1, q, k, v, gb, S, lens)
+    for i, m in enumerate(lens):
+        assert torch.isnan(out[i, m:]).all()
+
+
 def test_gdn_scan_and_forward_reach_one_state(K):
     """The state of kva_op_gdn_scan (16-bit operands, its own 1e-2) and of this operator."""
     T, nk, nv, d = 130, 2, 6, 128
