@@ -451,8 +451,10 @@ def _current_stream(dev: int) -> int:
     return torch.cuda.current_stream(dev).cuda_stream
 
 
-# the same without building a Stream object (1.2 us a call), where this torch has it
+# the same without building a Stream object (1.2 us a call), and the current device without looking whether CUDA
+# is up (with a tensor of it at hand it is), where this torch has them
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _one_device(stream, *tensors) -> tuple:
@@ -467,7 +469,7 @@ def _one_device(stream, *tensors) -> tuple:
 
 def _call_on(dev: int, what: str, fn, *args) -> None:
     """fn(*args) with device `dev` current, its status checked."""
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args)
     else:
         with torch.cuda.device(dev):
