@@ -188,7 +188,10 @@ __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constan
 // warps share a scheduler: fp16 301 us, bf16 with its units 357 us.  Measured and not kept (us for 1 / 8
 // sequences, against the state of that step): runs of 32 tokens (100 / 399 against 82 / 362), the columns
 // split over pairs of warps (76 / 450 against 68 / 349), the update fused with the next run's Y (75 / 380
-// against 68 / 349), readouts by warps of their own (69 / 363 against 66 / 349), and chunks of 64 tokens on
+// against 68 / 349), readouts by warps of their own (69 / 363 against 66 / 349), Tm diag(e^gam) K formed by the
+// preparing warps, so that U is V^T Tm^T less a product with S (78 / 387 against 66 / 357: the second term's
+// MMAs and loads cost more than the step they save), the next run's wait and first loads ahead of this one's
+// stores (69 / 370 against 66 / 357), and chunks of 64 tokens on
 // tcgen05 with the state in tensor memory (120 / 372 against 82 / 362): there every product makes a round
 // trip through tensor memory, 8 conversions a chunk at 0.5-2 k cycles, and an MMA takes about 96 cycles to
 // issue.
