@@ -24,6 +24,7 @@ struct GdnFwd {
   int T, n_k, n_v, has_lens;
   float scale;
   int* err;
+  int stall_run1;                  // test of the failure path: this run (from 1) is never handed over; 0: none
   int32_t lens[KVA_GDN_MAX_SEQ];
   uint8_t order[KVA_GDN_MAX_SEQ];  // with lens, in runs: the sequences, longest first
 };
@@ -391,7 +392,7 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
   for (int c = pw; c < n_runs; c += PREP) {
     const int cn = c + PREP * AHEAD;
     if (cn < n_runs) {
-      if (cn >= NST && !mbar_wait(&empty[cn % NST], (cn / NST - 1) & 1, abort_flag)) {
+      if (cn >= NST && !mbar_wait_warp(&empty[cn % NST], (cn / NST - 1) & 1, abort_flag)) {
         *abort_flag = 1;
         set_device_error(p.err, KVA_DEV_WAIT_TIMEOUT);
         break;
@@ -544,7 +545,7 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&full[c % NST]);
+    if (lane == 0 && c + 1 != p.stall_run1) mbar_arrive(&full[c % NST]);
   }
   cp_async_wait<0>();
 }
@@ -581,10 +582,10 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
   }
 
   for (int c = 0; c < n_runs; ++c) {
-    if (!mbar_wait(&full[c % NST], (c / NST) & 1, abort_flag)) {
+    if (!mbar_wait_warp(&full[c % NST], (c / NST) & 1, abort_flag)) {
       *abort_flag = 1;
       set_device_error(p.err, KVA_DEV_WAIT_TIMEOUT);
-      break;
+      return;  // (the state at hand is of no token that the caller knows: state_out stays as it was)
     }
     const uint8_t* st = sm + (c % NST) * St::BYTES;
     const uint32_t sst = base + (c % NST) * St::BYTES;
@@ -772,7 +773,7 @@ bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 }  // namespace
 }  // namespace kva
 
-extern "C" int kva_op_gdn_forward(const kva_gdn_forward_args* a, int32_t* err, void* stream) {
+static int gdn_forward(const kva_gdn_forward_args* a, int32_t* err, void* stream, int stall_run1) {
   using namespace kva;
   if (!a) return KVA_ERR_INVALID_ARG;
   if (a->dtype != KVA_BF16 && a->dtype != KVA_F16) return KVA_ERR_INVALID_ARG;
@@ -834,6 +835,7 @@ extern "C" int kva_op_gdn_forward(const kva_gdn_forward_args* a, int32_t* err, v
   p.n_v = a->n_v;
   p.scale = a->scale;
   p.err = err;
+  p.stall_run1 = stall_run1;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f16 = a->dtype == KVA_F16;
   const cudaError_t r = a->d == 128
@@ -842,4 +844,13 @@ extern "C" int kva_op_gdn_forward(const kva_gdn_forward_args* a, int32_t* err, v
                             : (f16 ? launch<__half, 64>(p, a->n_seq, longest, s)
                                    : launch<__nv_bfloat16, 64>(p, a->n_seq, longest, s));
   return r == cudaSuccess ? KVA_OK : KVA_ERR_CUDA;
+}
+
+extern "C" int kva_op_gdn_forward(const kva_gdn_forward_args* a, int32_t* err, void* stream) {
+  return gdn_forward(a, err, stream, 0);
+}
+
+extern "C" int kva_test_gdn_forward_wait_timeout(const kva_gdn_forward_args* a, int32_t* err, void* stream) {
+  if (!a || !err || a->T <= 32 || a->n_seq != 1 || a->lens) return KVA_ERR_INVALID_ARG;
+  return gdn_forward(a, err, stream, 2);
 }

@@ -143,6 +143,7 @@ def _load() -> C.CDLL:
         "kva_op_attention": (I32, [I32, P, I64, P, I64, I32, I32, I32, P]),
         "kva_op_gdn_scan": (I32, [P, P, P, P, I32, I32, I32, I32, I32, I32, P]),
         "kva_op_gdn_forward": (I32, [C.POINTER(KvaGdnForwardArgs), P, P]),
+        "kva_test_gdn_forward_wait_timeout": (I32, [C.POINTER(KvaGdnForwardArgs), P, P]),
         "kva_op_add_rmsnorm": (I32, [P, I32, I64, P, P, I32, I64, P, P, I32, I64, P, I32, I32, F32, P]),
         "kva_op_token_logprobs": (I32, [P, I32, I64, I32, I32, P, P, P, P, I32, P, P, P]),
         "kva_gdn_layer_update_noalloc": (I32, [P, I64, I32, I32, I32, I32, P, P, P, P, P, F32, P]),
@@ -164,7 +165,7 @@ EXPORTED = ("kva_init", "kva_workspace_bytes", "kva_prefill_ubatch", "kva_update
             "kva_op_rmsnorm", "kva_op_gemm", "kva_op_gemm_q8_0", "kva_op_gemm_q4_0", "kva_op_attention",
             "kva_op_gdn_scan", "kva_op_gdn_forward", "kva_op_add_rmsnorm", "kva_op_token_logprobs",
             "kva_gdn_layer_update_noalloc", "kva_gdn_layer_update_noalloc_status",
-            "kva_test_gemm_wait_timeout")
+            "kva_test_gemm_wait_timeout", "kva_test_gdn_forward_wait_timeout")
 
 
 def lib() -> C.CDLL:
@@ -506,7 +507,12 @@ def kva_op_gdn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gb: to
     dtype, each token's heads contiguous (views into a wider row are fine); gb fp32
     [n_seq, 2, n_v, T] (g, then beta); state_in and state_out fp32 [n_seq, n_v, d, d] (the same
     tensor: in place); lens: tokens of each sequence (host integers), default all T; err int32 [1]
-    receives device status bits."""
+    receives device status bits (without it a wait inside the kernel that gave up, which leaves out and
+    state_out undefined, is not reported)."""
+    _gdn_forward("kva_op_gdn_forward", q, k, v, gb, state_in, state_out, out, lens, scale, err, stream)
+
+
+def _gdn_forward(entry: str, q, k, v, gb, state_in, state_out, out, lens, scale, err, stream) -> None:
     qk_shape, dt = q.shape, q.dtype
     n_seq, T, n_k, d = qk_shape
     v_shape = (n_seq, T, v.shape[2], d)
@@ -539,7 +545,7 @@ def kva_op_gdn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gb: to
         _dense(state_in, S_shape, torch.float32, "state_in"),
         _dense(state_out, S_shape, torch.float32, "state_out"), out.data_ptr(), strides[6], strides[7],
         c_lens, scale)
-    _call_on(dev, "kva_op_gdn_forward", _lib.kva_op_gdn_forward, C.byref(a),
+    _call_on(dev, entry, getattr(_lib, entry), C.byref(a),
              _dense(err, (1,), torch.int32, "err"), s)
 
 
@@ -633,3 +639,11 @@ def kva_test_gemm_wait_timeout(A: torch.Tensor, B: torch.Tensor, D: torch.Tensor
     N = B.shape[0]
     _check(_lib.kva_test_gemm_wait_timeout(_DT[A.dtype], _ptr(A), _ptr(B), _ptr(D), M, N, K, _ptr(err),
                                            _stream(stream)), "kva_test_gemm_wait_timeout")
+
+
+def kva_test_gdn_forward_wait_timeout(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gb: torch.Tensor,
+                                      state_in: torch.Tensor, state_out: torch.Tensor, out: torch.Tensor,
+                                      err: torch.Tensor, stream=None) -> None:
+    """kva_op_gdn_forward of one sequence with a pipeline wait made to run out (see include/kva_ops.h):
+    the kernel must come back with KVA_DEV_WAIT_TIMEOUT in the device int `err`."""
+    _gdn_forward("kva_test_gdn_forward_wait_timeout", q, k, v, gb, state_in, state_out, out, None, 1.0, err, stream)

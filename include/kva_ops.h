@@ -149,7 +149,16 @@ typedef struct kva_gdn_forward_args {
                              the call: a captured graph keeps the lengths it was captured with. */
   float scale;            /* factor of the readout */
 } kva_gdn_forward_args;
+/* err: device int that takes status bits, or NULL.  A pipeline wait that gives up (after 2 s) sets
+ * KVA_DEV_WAIT_TIMEOUT there; out and state_out are then undefined (the blocks that gave up leave their
+ * rows of state_out as they were), and without err nothing reports it. */
 int kva_op_gdn_forward(const kva_gdn_forward_args* a, int32_t* err, void* stream);
+
+/* Test of the failure path of kva_op_gdn_forward; the method has no counterpart to it.  One sequence
+ * of more than 32 tokens (lens NULL) whose second run of 16 tokens is never handed to the warps that
+ * hold the state: their waits run out after 2 s and the kernel returns with KVA_DEV_WAIT_TIMEOUT set
+ * in *err and state_out as it was.  Nothing else runs on the stream meanwhile. */
+int kva_test_gdn_forward_wait_timeout(const kva_gdn_forward_args* a, int32_t* err, void* stream);
 
 /* The step between two layers: the residual stream takes a layer's output, and the next
  * layer's input is its RMSNorm.

@@ -46,6 +46,19 @@ def test_gdn_forward_nothing_to_do():
     assert _gdn(n_seq=0) == K.KVA_OK
 
 
+def test_gdn_wait_timeout_test_refuses():
+    """The test of the failure path takes one sequence of more than two runs, and a status to report to."""
+    def call(err=16, **kw):
+        a = K.KvaGdnForwardArgs(dtype=K.KVA_BF16, n_seq=1, T=33, n_k=2, n_v=4, d=64, q=16, k=16, v=16, gb=16,
+                                state_in=16, state_out=16, out=16, q_ld=128, k_ld=128, v_ld=256, out_ld=256, scale=1.0)
+        for n, x in kw.items():
+            setattr(a, n, x)
+        return K.lib().kva_test_gdn_forward_wait_timeout(C.byref(a), err, None)
+    for bad in (dict(err=None), dict(T=32), dict(n_seq=2), dict(n_seq=0), dict(lens=(C.c_int32 * 1)(33)), dict(q=None)):
+        assert call(**bad) == INVALID
+    assert K.lib().kva_test_gdn_forward_wait_timeout(None, 16, None) == INVALID
+
+
 def _norm(**kw):
     a = dict(x=16, x_dtype=K.KVA_F16, ldx=64, h=32, h_out=48, h_dtype=K.KVA_F32, ldh=64, g=64, out=80,
              out_dtype=K.KVA_BF16, ldo=64, scales=None, rows=3, n=64, eps=1e-6)
