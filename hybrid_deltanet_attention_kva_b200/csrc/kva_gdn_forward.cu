@@ -177,9 +177,9 @@ __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constan
 // no trip of S through shared or tensor memory.
 //
 // The state may not see a 16-bit rounding (it carries over thousands of tokens), so S, W, Tm and the
-// updates enter as two fp16 terms: two products where the partner is K, three where it has two terms
-// itself; the readout's Z takes S in one 16-bit term, rounded like the output.  That makes 94 MMAs a warp
-// and run (820 cycles of the tensor pipe alone).  bf16 inputs take fp16 terms as well, in units that
+// updates enter as two fp16 terms: two products where the partner is K or Q, three where it has two terms
+// itself.  So do S and M on the way to the readout, which sees one 16-bit rounding only, the output's.  That
+// makes 110 MMAs a warp and run.  bf16 inputs take fp16 terms as well, in units that
 // follow the data: two bf16 terms left states 3.4e-6 off after 1024 tokens (fp16 terms: 2e-7), three of
 // them would cost 30 % of the time, the units cost 4 to 9 %.
 //
@@ -208,11 +208,13 @@ struct Stage {
   static constexpr int V = Q + CH * D * 2;         // [16][ROWS], this block's columns
   static constexpr int TH = V + CH * ROWS * 2;     // Tm as two 16-bit terms, [s][t]
   static constexpr int TL = TH + CH * CH * 2;
-  static constexpr int MH = TL + CH * CH * 2;      // M as two 16-bit terms, [t][s]
+  static constexpr int MH = TL + CH * CH * 2;      // M as two 16-bit terms in units of MU, [t][s]
   static constexpr int ML = MH + CH * CH * 2;
   static constexpr int EG = ML + CH * CH * 2;      // e^gam[16]
   static constexpr int DEC = EG + CH * 4;          // e^(gam_last - gam)[16]
-  static constexpr int GL = DEC + CH * 4;          // e^gam_last, then (bf16) the largest |v|
+  static constexpr int EZ = DEC + CH * 4;          // e^gam[16] in q's units
+  static constexpr int MU = EZ + CH * 4;           // the units of M's rows
+  static constexpr int GL = MU + CH * 4;          // e^gam_last, then (bf16) the largest |v|
   static constexpr int BYTES = GL + 128;
 };
 struct Prep {                                      // per preparing warp: L in fp32 (row stride 20), beta
@@ -238,21 +240,14 @@ __device__ __forceinline__ uint32_t piece16(int r, int c) {
   return static_cast<uint32_t>(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
 }
 
-// x as two 16-bit terms, hi + lo.  fp16: hi is x cut to 11 bits, so that the remainder does not wait
-// for a conversion and back (x to 2^-21); bf16: hi is x rounded (x to 2^-16).
-template <typename T>
+// x as two fp16 terms, hi + lo: hi is x cut to 11 bits, so that the remainder does not wait for a
+// conversion and back (x to 2^-21)
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  if constexpr (F16<T>::umma_fmt == 0) {
-    const float2 h = make_float2(__uint_as_float(__float_as_uint(x) & 0xffffe000u),
-                                 __uint_as_float(__float_as_uint(y) & 0xffffe000u));
-    const float2 l = sub2(make_float2(x, y), h);
-    hi = F16<T>::pack(h.x, h.y);
-    lo = F16<T>::pack(l.x, l.y);
-  } else {
-    hi = F16<T>::pack(x, y);
-    const float2 l = sub2(make_float2(x, y), F16<T>::unpack(hi));
-    lo = F16<T>::pack(l.x, l.y);
-  }
+  const float2 h = make_float2(__uint_as_float(__float_as_uint(x) & 0xffffe000u),
+                               __uint_as_float(__float_as_uint(y) & 0xffffe000u));
+  const float2 l = sub2(make_float2(x, y), h);
+  hi = pack_f16(h.x, h.y);
+  lo = pack_f16(l.x, l.y);
 }
 // bf16 inputs: the chain's products are fp16 as well, in units of a power of two that follows the data.
 // What is at most m is below 2^8 in its units; with keys of norm <= 1 and beta <= 1, W, U and S of a run
@@ -298,13 +293,12 @@ __device__ __forceinline__ void scale_all(float (&x)[N][4], float f) {
     }
 }
 // accumulator fragments of two neighbouring 8-column tiles as an A operand (16 x 16)
-template <typename T>
 __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], uint32_t (&hi)[4],
                                         uint32_t (&lo)[4]) {
-  split2<T>(c0[0], c0[1], hi[0], lo[0]);
-  split2<T>(c0[2], c0[3], hi[1], lo[1]);
-  split2<T>(c1[0], c1[1], hi[2], lo[2]);
-  split2<T>(c1[2], c1[3], hi[3], lo[3]);
+  split2(c0[0], c0[1], hi[0], lo[0]);
+  split2(c0[2], c0[3], hi[1], lo[1]);
+  split2(c1[0], c1[1], hi[2], lo[2]);
+  split2(c1[2], c1[3], hi[3], lo[3]);
 }
 // D += A B on 16 x 8 x 16 tiles: registers to registers, free to be scheduled
 __device__ __forceinline__ void mma_tile(__half, float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -317,11 +311,41 @@ __device__ __forceinline__ void mma_tile(__nv_bfloat16, float (&d)[4], const uin
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <typename T>
+template <typename T = __half>
 __device__ __forceinline__ void mma2(float (&d0)[4], float (&d1)[4], const uint32_t (&a)[4], const uint32_t (&b)[4],
                                      int i0, int i1, int i2, int i3) {
   mma_tile(T(), d0, a, b[i0], b[i1]);
   mma_tile(T(), d1, a, b[i2], b[i3]);
+}
+
+// The rows of a [16][D] bf16 tile in fp16, each in units of a power of two that puts its largest entry
+// below 2^8 (exact but for entries below 2^-22 of that one); returns this lane's row's unit.  Two lanes take a
+// row, eight of whose neighbours' pieces fall on different banks.
+template <int D>
+__device__ __forceinline__ Scale rows_to_f16(uint8_t* tile, int lane) {
+  const int r = lane >> 1, h = lane & 1;
+  uint4 x[D / 16];
+  __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    x[j] = *reinterpret_cast<const uint4*>(tile + piece<2 * D>(r, (j & 3) | h << 2 | (j >> 2) << 3));
+    const __nv_bfloat162* x2 = reinterpret_cast<const __nv_bfloat162*>(&x[j]);
+    m = __hmax2(m, __hmax2(__hmax2(__habs2(x2[0]), __habs2(x2[1])), __hmax2(__habs2(x2[2]), __habs2(x2[3]))));
+  }
+  float big = fmaxf(__low2float(m), __high2float(m));
+  big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+  const Scale sc(big);
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&x[j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = mul2(unpack_bf16(w[i]), make_float2(sc.down, sc.down));
+      w[i] = pack_f16(f.x, f.y);
+    }
+    *reinterpret_cast<uint4*>(tile + piece<2 * D>(r, (j & 3) | h << 2 | (j >> 2) << 3)) = x[j];
+  }
+  return sc;
 }
 
 // A preparing warp: runs pw, pw + PREP, ...
@@ -454,6 +478,47 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
       mma2<T>(kk[0], kk[1], a, a, 0, 2, 1, 3);
       mma2<T>(qk[0], qk[1], x, a, 0, 2, 1, 3);
     }
+    // M, and the units of its rows: bf16, those of the query, whose row the chain's products take in fp16 too;
+    // fp16, from M's own largest entry
+    float mm[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // (pd is 0 above the diagonal, but 0 times an infinite product would not be)
+        const int s = 8 * i + 2 * cq + e;
+        mm[i][e] = s <= gr ? pd[i][e] * qk[i][e] : 0.f;
+        mm[i][2 + e] = s <= gr + 8 ? pd[i][2 + e] * qk[i][2 + e] : 0.f;
+      }
+    float ez = expf(gam + gaml), m0, m1;  // the factors that take M's rows to their units
+    if constexpr (kScaled<T>) {
+      __syncwarp();
+      const Scale sq = rows_to_f16<D>(st + St::Q, lane);
+      m0 = __shfl_sync(0xffffffffu, sq.down, 2 * gr);
+      m1 = __shfl_sync(0xffffffffu, sq.down, 2 * gr + 16);
+      const float up = __shfl_sync(0xffffffffu, sq.up, 2 * (lane & 15));
+      if (lane < CH) reinterpret_cast<float*>(st + St::MU)[lane] = up;
+      ez *= up;
+    } else {
+      float b0 = 0.f, b1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        b0 = fmaxf(b0, fmaxf(fabsf(mm[i][0]), fabsf(mm[i][1])));
+        b1 = fmaxf(b1, fmaxf(fabsf(mm[i][2]), fabsf(mm[i][3])));
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, o));
+        b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, o));
+      }
+      const Scale s0(b0), s1(b1);
+      m0 = s0.down;
+      m1 = s1.down;
+      if (cq == 0) {
+        reinterpret_cast<float*>(st + St::MU)[gr] = s0.up;
+        reinterpret_cast<float*>(st + St::MU)[gr + 8] = s1.up;
+      }
+    }
+    if (lane < CH) reinterpret_cast<float*>(st + St::EZ)[lane] = ez;
     const float bt0 = __shfl_sync(0xffffffffu, bt, gr), bt1 = __shfl_sync(0xffffffffu, bt, gr + 8);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -462,12 +527,11 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
           make_float2(s < gr ? bt0 * pd[i][0] * kk[i][0] : 0.f, s + 1 < gr ? bt0 * pd[i][1] * kk[i][1] : 0.f);
       *reinterpret_cast<float2*>(Ls + (gr + 8) * Prep::LDL + s) =
           make_float2(s < gr + 8 ? bt1 * pd[i][2] * kk[i][2] : 0.f, s + 1 < gr + 8 ? bt1 * pd[i][3] * kk[i][3] : 0.f);
-      // (pd is 0 above the diagonal, but 0 times an infinite product would not be)
       uint32_t hi, lo;
-      split2<T>(s <= gr ? pd[i][0] * qk[i][0] : 0.f, s + 1 <= gr ? pd[i][1] * qk[i][1] : 0.f, hi, lo);
+      split2(mm[i][0] * m0, mm[i][1] * m0, hi, lo);
       *reinterpret_cast<uint32_t*>(st + St::MH + piece16(gr, i) + 4 * cq) = hi;
       *reinterpret_cast<uint32_t*>(st + St::ML + piece16(gr, i) + 4 * cq) = lo;
-      split2<T>(s <= gr + 8 ? pd[i][2] * qk[i][2] : 0.f, s + 1 <= gr + 8 ? pd[i][3] * qk[i][3] : 0.f, hi, lo);
+      split2(mm[i][2] * m1, mm[i][3] * m1, hi, lo);
       *reinterpret_cast<uint32_t*>(st + St::MH + piece16(gr + 8, i) + 4 * cq) = hi;
       *reinterpret_cast<uint32_t*>(st + St::ML + piece16(gr + 8, i) + 4 * cq) = lo;
     }
@@ -505,7 +569,7 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          split2<__half>(x[8 * i + 2 * j] * bb[8 * i + 2 * j], x[8 * i + 2 * j + 1] * bb[8 * i + 2 * j + 1], hi[j], lo[j]);
+          split2(x[8 * i + 2 * j] * bb[8 * i + 2 * j], x[8 * i + 2 * j + 1] * bb[8 * i + 2 * j + 1], hi[j], lo[j]);
         *reinterpret_cast<uint4*>(st + St::TH + piece16(lane, i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(st + St::TL + piece16(lane, i)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
@@ -589,8 +653,8 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
     }
     const uint8_t* st = sm + (c % NST) * St::BYTES;
     const uint32_t sst = base + (c % NST) * St::BYTES;
-    // Y = S K^T (both terms of S), Z = S Q^T (the first term)
-    float y[2][4] = {}, yl[2][4] = {}, z[2][4] = {};
+    // Y = S K^T, Z = S Q^T, both terms of S (the second's products apart: shorter chains)
+    float y[2][4] = {}, yl[2][4] = {}, z[2][4] = {}, zl[2][4] = {};
     uint32_t kf[2][4], qf[2][4];
     ldmatrix_x4(kf[0], sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, mi >> 1));
     ldmatrix_x4(qf[0], sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, mi >> 1));
@@ -601,17 +665,11 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
         ldmatrix_x4(qf[(ks + 1) & 1], sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + 2 + (mi >> 1)));
       }
       uint32_t ah[4], al[4];
-      split_a<__half>(S[2 * ks], S[2 * ks + 1], ah, al);
-      mma2<__half>(y[0], y[1], ah, kf[ks & 1], 0, 2, 1, 3);
-      mma2<__half>(yl[0], yl[1], al, kf[ks & 1], 0, 2, 1, 3);
-      if constexpr (kScaled<T>) {  // (q may be anything: it stays bf16)
-        const float(&s0)[4] = S[2 * ks], (&s1)[4] = S[2 * ks + 1];
-        const uint32_t az[4] = {F16<T>::pack(s0[0], s0[1]), F16<T>::pack(s0[2], s0[3]), F16<T>::pack(s1[0], s1[1]),
-                                F16<T>::pack(s1[2], s1[3])};
-        mma2<T>(z[0], z[1], az, qf[ks & 1], 0, 2, 1, 3);
-      } else {
-        mma2<T>(z[0], z[1], ah, qf[ks & 1], 0, 2, 1, 3);
-      }
+      split_a(S[2 * ks], S[2 * ks + 1], ah, al);
+      mma2(y[0], y[1], ah, kf[ks & 1], 0, 2, 1, 3);
+      mma2(yl[0], yl[1], al, kf[ks & 1], 0, 2, 1, 3);
+      mma2(z[0], z[1], ah, qf[ks & 1], 0, 2, 1, 3);
+      mma2(zl[0], zl[1], al, qf[ks & 1], 0, 2, 1, 3);
     }
     // W = V^T - Y diag(e^gam)
     uint32_t vf[4], wh[4], wl[4];
@@ -631,28 +689,32 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float2 e = *reinterpret_cast<const float2*>(st + St::EG + (8 * i + 2 * cq) * 4);
-      if constexpr (kScaled<T>) e = mul2(e, make_float2(up, up));
+      float2 ez = *reinterpret_cast<const float2*>(st + St::EZ + (8 * i + 2 * cq) * 4);
+      if constexpr (kScaled<T>) {
+        e = mul2(e, make_float2(up, up));
+        ez = mul2(ez, make_float2(up, up));
+      }
       const float2 v0 = F16<T>::unpack(vf[2 * i]), v1 = F16<T>::unpack(vf[2 * i + 1]);
       w[i][0] = v0.x - e.x * (y[i][0] + yl[i][0]);
       w[i][1] = v0.y - e.y * (y[i][1] + yl[i][1]);
       w[i][2] = v1.x - e.x * (y[i][2] + yl[i][2]);
       w[i][3] = v1.y - e.y * (y[i][3] + yl[i][3]);
-      z[i][0] *= e.x;
-      z[i][1] *= e.y;
-      z[i][2] *= e.x;
-      z[i][3] *= e.y;
+      z[i][0] = ez.x * (z[i][0] + zl[i][0]);
+      z[i][1] = ez.y * (z[i][1] + zl[i][1]);
+      z[i][2] = ez.x * (z[i][2] + zl[i][2]);
+      z[i][3] = ez.y * (z[i][3] + zl[i][3]);
     }
     if constexpr (kScaled<T>) scale_all(w, sc.down);
-    split_a<__half>(w[0], w[1], wh, wl);
+    split_a(w[0], w[1], wh, wl);
     // U = W Tm^T
     float u[2][4] = {}, ul[2][4] = {};
     {
       uint32_t th[4], tl[4];
       ldmatrix_x4(th, sst + St::TH + piece16((mi & 1) * 8 + lr, mi >> 1));
       ldmatrix_x4(tl, sst + St::TL + piece16((mi & 1) * 8 + lr, mi >> 1));
-      mma2<__half>(u[0], u[1], wh, th, 0, 2, 1, 3);
-      mma2<__half>(ul[0], ul[1], wl, th, 0, 2, 1, 3);
-      mma2<__half>(ul[0], ul[1], wh, tl, 0, 2, 1, 3);
+      mma2(u[0], u[1], wh, th, 0, 2, 1, 3);
+      mma2(ul[0], ul[1], wl, th, 0, 2, 1, 3);
+      mma2(ul[0], ul[1], wh, tl, 0, 2, 1, 3);
     }
     uint32_t uh[4], uo[4], dh[4], dl[4];
     {
@@ -667,9 +729,8 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
         dd[i][2] = u[i][2] * e.x;
         dd[i][3] = u[i][3] * e.y;
       }
-      split_a<__half>(dd[0], dd[1], dh, dl);
-      if constexpr (kScaled<T>) scale_all(u, sc.up);
-      split_a<T>(u[0], u[1], uh, uo);
+      split_a(dd[0], dd[1], dh, dl);
+      split_a(u[0], u[1], uh, uo);
     }
     // S <- e^gam_last S + U diag(dec) K
     scale_all(S, decay);
@@ -677,18 +738,28 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
     for (int ks = 0; ks < D / 16; ++ks) {
       uint32_t kt[4];
       ldmatrix_x4_trans(kt, sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
-      mma2<__half>(S[2 * ks], S[2 * ks + 1], dh, kt, 0, 1, 2, 3);
-      mma2<__half>(S[2 * ks], S[2 * ks + 1], dl, kt, 0, 1, 2, 3);
+      mma2(S[2 * ks], S[2 * ks + 1], dh, kt, 0, 1, 2, 3);
+      mma2(S[2 * ks], S[2 * ks + 1], dl, kt, 0, 1, 2, 3);
     }
     if (kScaled<T> && (c & 7) == 7) norm = fminf(norm, root * sc.up * warp_largest(S));
     // O = Z diag(e^gam) + U M^T, written token-major
     {
       uint32_t mh[4], ml[4];
+      float o[2][4] = {};
       ldmatrix_x4(mh, sst + St::MH + piece16((mi & 1) * 8 + lr, mi >> 1));
       ldmatrix_x4(ml, sst + St::ML + piece16((mi & 1) * 8 + lr, mi >> 1));
-      mma2<T>(z[0], z[1], uh, mh, 0, 2, 1, 3);
-      mma2<T>(z[0], z[1], uo, mh, 0, 2, 1, 3);
-      mma2<T>(z[0], z[1], uh, ml, 0, 2, 1, 3);
+      mma2(o[0], o[1], uh, mh, 0, 2, 1, 3);
+      mma2(o[0], o[1], uo, mh, 0, 2, 1, 3);
+      mma2(o[0], o[1], uh, ml, 0, 2, 1, 3);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float2 mu = *reinterpret_cast<const float2*>(st + St::MU + (8 * i + 2 * cq) * 4);
+        if constexpr (kScaled<T>) mu = mul2(mu, make_float2(sc.up, sc.up));
+        z[i][0] = fmaf(mu.x, o[i][0], z[i][0]);
+        z[i][1] = fmaf(mu.y, o[i][1], z[i][1]);
+        z[i][2] = fmaf(mu.x, o[i][2], z[i][2]);
+        z[i][3] = fmaf(mu.y, o[i][3], z[i][3]);
+      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[c % NST]);

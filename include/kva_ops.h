@@ -120,8 +120,7 @@ int kva_op_gdn_scan(const void* k, const void* v, const float* gb, float* state,
  *   o_t = scale * S_t q_t
  * v head h reads k and q head h / (n_v / n_k).  The state is held in fp32 throughout.
  * Up to 8 tokens run one after the other in fp32; longer sequences in runs of 16 on the tensor
- * cores, where fp32 operands enter as the sum of two fp16 values (an error of 2^-21 relative; the
- * state's part of a readout as one value of `dtype`).  With KVA_F16 the state and v - S k must then
+ * cores, where fp32 operands enter as the sum of two fp16 values (an error of 2^-21 relative).  With KVA_F16 the state and v - S k must then
  * stay below 65504.  With KVA_BF16 the fp16 values are in units of a power of two that follows
  * the data, and what is below 2^-32 of the largest v of a run and the state's rows before it is
  * dropped: any state and v up to 1e30 work, given 0 <= beta <= 1.  A NaN or an infinity in a
