@@ -60,6 +60,11 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         "l"(reinterpret_cast<unsigned long long&>(c)));
   return d;
 }
+__device__ __forceinline__ float sum4(float v) {  // over the 4 lanes of a fragment's row
+  v += __shfl_xor_sync(0xffffffffu, v, 2);
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v;
+}
 __device__ __forceinline__ float sum8(float v) {  // over the 8 lanes of a row
   v += __shfl_xor_sync(0xffffffffu, v, 4);
   v += __shfl_xor_sync(0xffffffffu, v, 2);
@@ -214,7 +219,7 @@ struct Stage {
   static constexpr int DEC = EG + CH * 4;          // e^(gam_last - gam)[16]
   static constexpr int EZ = DEC + CH * 4;          // e^gam[16] in q's units
   static constexpr int MU = EZ + CH * 4;           // the units of M's rows
-  static constexpr int GL = MU + CH * 4;          // e^gam_last, then (bf16) the largest |v|
+  static constexpr int GL = MU + CH * 4;          // e^gam_last, (bf16) largest |v| and e^gam_t; 1: ordinary run
   static constexpr int BYTES = GL + 128;
 };
 struct Prep {                                      // per preparing warp: L in fp32 (row stride 20), beta
@@ -250,9 +255,14 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = pack_f16(l.x, l.y);
 }
 // bf16 inputs: the chain's products are fp16 as well, in units of a power of two that follows the data.
-// What is at most m is below 2^8 in its units; with keys of norm <= 1 and beta <= 1, W, U and S of a run
-// whose values are at most m and whose state rows have a norm of at most m stay below 18 m: below fp16's
-// 65504, and what fp16 drops is 2^-32 m.
+// What is at most m is below 2^8 in its units.  m is the largest of a run's |v| and of the decayed norms
+// e^gam_t |S row| in which its tokens meet the state (the state at the run's end may be far below those);
+// with keys of norm <= 1 and beta <= 1, W, U and S of the run stay below 18 m: below fp16's 65504, and what
+// fp16 drops is 2^-32 m.  A run that ends far below m (strong decay of a state with little written to it)
+// would lose its own precision by that, and gates or keys out of their range could pass 18 m: such runs go
+// token by token in fp32 (step_tokens).
+constexpr float kFar = 256.f;        // m over the larger of |v| and the state's norm behind the run: 2^-24 of those
+constexpr float kKeyNorm2 = 1.015625f;  // keys of norm 1, each entry rounded to bf16
 template <typename T>
 constexpr bool kScaled = F16<T>::umma_fmt == 1;
 struct Scale {
@@ -426,6 +436,7 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
     cp_async_commit();
     float gt = g_next;
     const float bt = b_next;
+    bool ordinary = gt <= 0.f && bt >= 0.f && bt <= 1.f;
     load_gates(c + PREP);  // (past the last run: zeros)
     // e^g is 0 in fp32 from -104 on; the clamp keeps -infinity out of the differences
     gt = gt < -1000.f ? -1000.f : gt;
@@ -477,6 +488,11 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
       ldmatrix_x4(x, sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
       mma2<T>(kk[0], kk[1], a, a, 0, 2, 1, 3);
       mma2<T>(qk[0], qk[1], x, a, 0, 2, 1, 3);
+    }
+    {
+      const float k0 = gr & 1 ? kk[0][1] : kk[0][0], k1 = gr & 1 ? kk[1][3] : kk[1][2];  // |k_t|^2, t = gr, gr + 8
+      ordinary = __all_sync(0xffffffffu, ordinary && (cq != gr >> 1 || (k0 <= kKeyNorm2 && k1 <= kKeyNorm2)));
+      if (lane == 0) reinterpret_cast<float*>(st + St::GL)[3] = ordinary ? 1.f : 0.f;
     }
     // M, and the units of its rows: bf16, those of the query, whose row the chain's products take in fp16 too;
     // fp16, from M's own largest entry
@@ -593,7 +609,12 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
         }
         big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
       }
-      if (lane == 0) *reinterpret_cast<float*>(st + St::GL + 4) = big;
+      float decay = lane < CH ? reinterpret_cast<const float*>(st + St::EG)[lane] : 0.f;  // (NaN counts as the largest)
+      decay = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(decay)));
+      if (lane == 0) {
+        reinterpret_cast<float*>(st + St::GL)[1] = big;
+        reinterpret_cast<float*>(st + St::GL)[2] = decay;
+      }
       // the chain's products take K in fp16: exact but for what is below 2^-17
 #pragma unroll 2
       for (int i = lane; i < CH * D / 8; i += 32) {
@@ -612,6 +633,67 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
     if (lane == 0 && c + 1 != p.stall_run1) mbar_arrive(&full[c % NST]);
   }
   cp_async_wait<0>();
+}
+
+// n tokens from t0 on, one after the other in fp32, for the rows of a chain warp: a run that fp16 terms in one
+// unit cannot hold.  `state`: a lane's fragments of S in true size; `row`: its first row of the head.  (Out of
+// line, as between the runs' steps its instructions cost them 6 %: 8 sequences 412 against 394 us.)
+template <typename T, int D>
+__device__ __noinline__ void step_tokens(const GdnFwd& p, float* state, int h, int row, int seq, int t0, int n,
+                                         int lane) {
+  float S[D / 8][4];
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[j][e] = state[4 * j + e];
+  const int cq = lane & 3, kh = h / (p.n_v / p.n_k);
+  const T* k = static_cast<const T*>(p.k) + seq * p.k_seq + t0 * p.k_ld + kh * D + 2 * cq;
+  const T* q = static_cast<const T*>(p.q) + seq * p.q_seq + t0 * p.q_ld + kh * D + 2 * cq;
+  const T* v = static_cast<const T*>(p.v) + seq * p.v_seq + t0 * p.v_ld + h * D + row;
+  T* out = static_cast<T*>(p.out) + seq * p.out_seq + t0 * p.out_ld + h * D + row;
+  const float* g = p.gb + (static_cast<int64_t>(seq) * 2 * p.n_v + h) * p.T + t0;
+  for (int t = 0; t < n; ++t) {
+    const float dec = expf(g[t]), beta = g[static_cast<int64_t>(p.n_v) * p.T + t];
+    uint32_t kk[D / 8];
+    float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) kk[j] = *reinterpret_cast<const uint32_t*>(k + 8 * j);
+    scale_all(S, dec);
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) {
+      const float2 f = F16<T>::unpack(kk[j]);
+      a0 = fma2(make_float2(S[j][0], S[j][1]), f, a0);
+      a1 = fma2(make_float2(S[j][2], S[j][3]), f, a1);
+    }
+    const float u0 = beta * (F16<T>::to(v[0]) - sum4(a0.x + a0.y));
+    const float u1 = beta * (F16<T>::to(v[8]) - sum4(a1.x + a1.y));
+    a0 = a1 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) {
+      const float2 f = F16<T>::unpack(kk[j]), qf = F16<T>::unpack(*reinterpret_cast<const uint32_t*>(q + 8 * j));
+      const float2 s0 = fma2(make_float2(u0, u0), f, make_float2(S[j][0], S[j][1]));
+      const float2 s1 = fma2(make_float2(u1, u1), f, make_float2(S[j][2], S[j][3]));
+      a0 = fma2(s0, qf, a0);
+      a1 = fma2(s1, qf, a1);
+      S[j][0] = s0.x;
+      S[j][1] = s0.y;
+      S[j][2] = s1.x;
+      S[j][3] = s1.y;
+    }
+    const float o0 = sum4(a0.x + a0.y), o1 = sum4(a1.x + a1.y);
+    if (cq == 0) {
+      out[0] = F16<T>::from(p.scale * o0);
+      out[8] = F16<T>::from(p.scale * o1);
+    }
+    k += p.k_ld;
+    q += p.q_ld;
+    v += p.v_ld;
+    out += p.out_ld;
+  }
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) state[4 * j + e] = S[j][e];
 }
 
 template <typename T, int D, int ROWS, int PREP>
@@ -645,134 +727,159 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
     scale_all(S, sc.down);
   }
 
-  for (int c = 0; c < n_runs; ++c) {
-    if (!mbar_wait_warp(&full[c % NST], (c / NST) & 1, abort_flag)) {
-      *abort_flag = 1;
-      set_device_error(p.err, KVA_DEV_WAIT_TIMEOUT);
-      return;  // (the state at hand is of no token that the caller knows: state_out stays as it was)
-    }
-    const uint8_t* st = sm + (c % NST) * St::BYTES;
-    const uint32_t sst = base + (c % NST) * St::BYTES;
-    // Y = S K^T, Z = S Q^T, both terms of S (the second's products apart: shorter chains)
-    float y[2][4] = {}, yl[2][4] = {}, z[2][4] = {}, zl[2][4] = {};
-    uint32_t kf[2][4], qf[2][4];
-    ldmatrix_x4(kf[0], sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, mi >> 1));
-    ldmatrix_x4(qf[0], sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, mi >> 1));
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      if (ks + 1 < D / 16) {
-        ldmatrix_x4(kf[(ks + 1) & 1], sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + 2 + (mi >> 1)));
-        ldmatrix_x4(qf[(ks + 1) & 1], sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + 2 + (mi >> 1)));
+  int c = 0;
+  while (true) {
+    for (; c < n_runs; ++c) {
+      if (!mbar_wait_warp(&full[c % NST], (c / NST) & 1, abort_flag)) {
+        *abort_flag = 1;
+        set_device_error(p.err, KVA_DEV_WAIT_TIMEOUT);
+        return;  // (the state at hand is of no token that the caller knows: state_out stays as it was)
       }
-      uint32_t ah[4], al[4];
-      split_a(S[2 * ks], S[2 * ks + 1], ah, al);
-      mma2(y[0], y[1], ah, kf[ks & 1], 0, 2, 1, 3);
-      mma2(yl[0], yl[1], al, kf[ks & 1], 0, 2, 1, 3);
-      mma2(z[0], z[1], ah, qf[ks & 1], 0, 2, 1, 3);
-      mma2(zl[0], zl[1], al, qf[ks & 1], 0, 2, 1, 3);
-    }
-    // W = V^T - Y diag(e^gam)
-    uint32_t vf[4], wh[4], wl[4];
-    ldmatrix_x4_trans(vf, sst + St::V + piece<2 * ROWS>((mi >> 1) * 8 + lr, 2 * warp + (mi & 1)));
-    const float2 gv = *reinterpret_cast<const float2*>(st + St::GL);
-    float decay = gv.x, up = 1.f;  // of S into the next run; the units of Y and Z
-    if constexpr (kScaled<T>) {
-      // the run's units, from its values and the state's decayed rows
-      up = sc.up;
-      const Scale now(fmaxf(gv.y, gv.x * norm));
-      decay *= sc.up * now.down;
-      sc = now;
-      // S <- e^g S (I - beta k k^T) + beta v k^T, 16 times
-      norm = fmaf(16.f, gv.y, gv.x * norm);
-    }
-    float w[2][4];
+      const uint8_t* st = sm + (c % NST) * St::BYTES;
+      const uint32_t sst = base + (c % NST) * St::BYTES;
+      const float4 gv = *reinterpret_cast<const float4*>(st + St::GL);
+      // (the same for the whole warp)
+      if (gv.w == 0.f || (kScaled<T> && gv.z * norm > kFar * fmaxf(gv.y, gv.x * norm))) break;
+      // Y = S K^T, Z = S Q^T, both terms of S (the second's products apart: shorter chains)
+      float y[2][4] = {}, yl[2][4] = {}, z[2][4] = {}, zl[2][4] = {};
+      uint32_t kf[2][4], qf[2][4];
+      ldmatrix_x4(kf[0], sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, mi >> 1));
+      ldmatrix_x4(qf[0], sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, mi >> 1));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float2 e = *reinterpret_cast<const float2*>(st + St::EG + (8 * i + 2 * cq) * 4);
-      float2 ez = *reinterpret_cast<const float2*>(st + St::EZ + (8 * i + 2 * cq) * 4);
+      for (int ks = 0; ks < D / 16; ++ks) {
+        if (ks + 1 < D / 16) {
+          ldmatrix_x4(kf[(ks + 1) & 1], sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + 2 + (mi >> 1)));
+          ldmatrix_x4(qf[(ks + 1) & 1], sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + 2 + (mi >> 1)));
+        }
+        uint32_t ah[4], al[4];
+        split_a(S[2 * ks], S[2 * ks + 1], ah, al);
+        mma2(y[0], y[1], ah, kf[ks & 1], 0, 2, 1, 3);
+        mma2(yl[0], yl[1], al, kf[ks & 1], 0, 2, 1, 3);
+        mma2(z[0], z[1], ah, qf[ks & 1], 0, 2, 1, 3);
+        mma2(zl[0], zl[1], al, qf[ks & 1], 0, 2, 1, 3);
+      }
+      // W = V^T - Y diag(e^gam)
+      uint32_t vf[4], wh[4], wl[4];
+      ldmatrix_x4_trans(vf, sst + St::V + piece<2 * ROWS>((mi >> 1) * 8 + lr, 2 * warp + (mi & 1)));
+      float decay = gv.x, up = 1.f;  // of S into the next run; the units of Y and Z
       if constexpr (kScaled<T>) {
-        e = mul2(e, make_float2(up, up));
-        ez = mul2(ez, make_float2(up, up));
+        // the run's units, from its values and the state's rows as its tokens meet them
+        up = sc.up;
+        const Scale now(fmaxf(gv.y, gv.z * norm));
+        decay *= sc.up * now.down;
+        sc = now;
+        // S <- e^g S (I - beta k k^T) + beta v k^T, 16 times
+        norm = fmaf(16.25f, gv.y, gv.x * norm);
       }
-      const float2 v0 = F16<T>::unpack(vf[2 * i]), v1 = F16<T>::unpack(vf[2 * i + 1]);
-      w[i][0] = v0.x - e.x * (y[i][0] + yl[i][0]);
-      w[i][1] = v0.y - e.y * (y[i][1] + yl[i][1]);
-      w[i][2] = v1.x - e.x * (y[i][2] + yl[i][2]);
-      w[i][3] = v1.y - e.y * (y[i][3] + yl[i][3]);
-      z[i][0] = ez.x * (z[i][0] + zl[i][0]);
-      z[i][1] = ez.y * (z[i][1] + zl[i][1]);
-      z[i][2] = ez.x * (z[i][2] + zl[i][2]);
-      z[i][3] = ez.y * (z[i][3] + zl[i][3]);
-    }
-    if constexpr (kScaled<T>) scale_all(w, sc.down);
-    split_a(w[0], w[1], wh, wl);
-    // U = W Tm^T
-    float u[2][4] = {}, ul[2][4] = {};
-    {
-      uint32_t th[4], tl[4];
-      ldmatrix_x4(th, sst + St::TH + piece16((mi & 1) * 8 + lr, mi >> 1));
-      ldmatrix_x4(tl, sst + St::TL + piece16((mi & 1) * 8 + lr, mi >> 1));
-      mma2(u[0], u[1], wh, th, 0, 2, 1, 3);
-      mma2(ul[0], ul[1], wl, th, 0, 2, 1, 3);
-      mma2(ul[0], ul[1], wh, tl, 0, 2, 1, 3);
-    }
-    uint32_t uh[4], uo[4], dh[4], dl[4];
-    {
-      float dd[2][4];
+      float w[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float2 e = *reinterpret_cast<const float2*>(st + St::DEC + (8 * i + 2 * cq) * 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u[i][j] += ul[i][j];
-        dd[i][0] = u[i][0] * e.x;
-        dd[i][1] = u[i][1] * e.y;
-        dd[i][2] = u[i][2] * e.x;
-        dd[i][3] = u[i][3] * e.y;
+        float2 e = *reinterpret_cast<const float2*>(st + St::EG + (8 * i + 2 * cq) * 4);
+        float2 ez = *reinterpret_cast<const float2*>(st + St::EZ + (8 * i + 2 * cq) * 4);
+        if constexpr (kScaled<T>) {
+          e = mul2(e, make_float2(up, up));
+          ez = mul2(ez, make_float2(up, up));
+        }
+        const float2 v0 = F16<T>::unpack(vf[2 * i]), v1 = F16<T>::unpack(vf[2 * i + 1]);
+        w[i][0] = v0.x - e.x * (y[i][0] + yl[i][0]);
+        w[i][1] = v0.y - e.y * (y[i][1] + yl[i][1]);
+        w[i][2] = v1.x - e.x * (y[i][2] + yl[i][2]);
+        w[i][3] = v1.y - e.y * (y[i][3] + yl[i][3]);
+        z[i][0] = ez.x * (z[i][0] + zl[i][0]);
+        z[i][1] = ez.y * (z[i][1] + zl[i][1]);
+        z[i][2] = ez.x * (z[i][2] + zl[i][2]);
+        z[i][3] = ez.y * (z[i][3] + zl[i][3]);
       }
-      split_a(dd[0], dd[1], dh, dl);
-      split_a(u[0], u[1], uh, uo);
-    }
-    // S <- e^gam_last S + U diag(dec) K
-    scale_all(S, decay);
+      if constexpr (kScaled<T>) scale_all(w, sc.down);
+      split_a(w[0], w[1], wh, wl);
+      // U = W Tm^T
+      float u[2][4] = {}, ul[2][4] = {};
+      {
+        uint32_t th[4], tl[4];
+        ldmatrix_x4(th, sst + St::TH + piece16((mi & 1) * 8 + lr, mi >> 1));
+        ldmatrix_x4(tl, sst + St::TL + piece16((mi & 1) * 8 + lr, mi >> 1));
+        mma2(u[0], u[1], wh, th, 0, 2, 1, 3);
+        mma2(ul[0], ul[1], wl, th, 0, 2, 1, 3);
+        mma2(ul[0], ul[1], wh, tl, 0, 2, 1, 3);
+      }
+      uint32_t uh[4], uo[4], dh[4], dl[4];
+      {
+        float dd[2][4];
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t kt[4];
-      ldmatrix_x4_trans(kt, sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
-      mma2(S[2 * ks], S[2 * ks + 1], dh, kt, 0, 1, 2, 3);
-      mma2(S[2 * ks], S[2 * ks + 1], dl, kt, 0, 1, 2, 3);
-    }
-    if (kScaled<T> && (c & 7) == 7) norm = fminf(norm, root * sc.up * warp_largest(S));
-    // O = Z diag(e^gam) + U M^T, written token-major
-    {
-      uint32_t mh[4], ml[4];
-      float o[2][4] = {};
-      ldmatrix_x4(mh, sst + St::MH + piece16((mi & 1) * 8 + lr, mi >> 1));
-      ldmatrix_x4(ml, sst + St::ML + piece16((mi & 1) * 8 + lr, mi >> 1));
-      mma2(o[0], o[1], uh, mh, 0, 2, 1, 3);
-      mma2(o[0], o[1], uo, mh, 0, 2, 1, 3);
-      mma2(o[0], o[1], uh, ml, 0, 2, 1, 3);
+        for (int i = 0; i < 2; ++i) {
+          const float2 e = *reinterpret_cast<const float2*>(st + St::DEC + (8 * i + 2 * cq) * 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[i][j] += ul[i][j];
+          dd[i][0] = u[i][0] * e.x;
+          dd[i][1] = u[i][1] * e.y;
+          dd[i][2] = u[i][2] * e.x;
+          dd[i][3] = u[i][3] * e.y;
+        }
+        split_a(dd[0], dd[1], dh, dl);
+        split_a(u[0], u[1], uh, uo);
+      }
+      // S <- e^gam_last S + U diag(dec) K
+      scale_all(S, decay);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t kt[4];
+        ldmatrix_x4_trans(kt, sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, 2 * ks + (mi >> 1)));
+        mma2(S[2 * ks], S[2 * ks + 1], dh, kt, 0, 1, 2, 3);
+        mma2(S[2 * ks], S[2 * ks + 1], dl, kt, 0, 1, 2, 3);
+      }
+      if (kScaled<T> && (c & 7) == 7) norm = fminf(norm, root * sc.up * warp_largest(S));
+      // O = Z diag(e^gam) + U M^T, written token-major
+      {
+        uint32_t mh[4], ml[4];
+        float o[2][4] = {};
+        ldmatrix_x4(mh, sst + St::MH + piece16((mi & 1) * 8 + lr, mi >> 1));
+        ldmatrix_x4(ml, sst + St::ML + piece16((mi & 1) * 8 + lr, mi >> 1));
+        mma2(o[0], o[1], uh, mh, 0, 2, 1, 3);
+        mma2(o[0], o[1], uo, mh, 0, 2, 1, 3);
+        mma2(o[0], o[1], uh, ml, 0, 2, 1, 3);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float2 mu = *reinterpret_cast<const float2*>(st + St::MU + (8 * i + 2 * cq) * 4);
+          if constexpr (kScaled<T>) mu = mul2(mu, make_float2(sc.up, sc.up));
+          z[i][0] = fmaf(mu.x, o[i][0], z[i][0]);
+          z[i][1] = fmaf(mu.y, o[i][1], z[i][1]);
+          z[i][2] = fmaf(mu.x, o[i][2], z[i][2]);
+          z[i][3] = fmaf(mu.y, o[i][3], z[i][3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[c % NST]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float2 mu = *reinterpret_cast<const float2*>(st + St::MU + (8 * i + 2 * cq) * 4);
-        if constexpr (kScaled<T>) mu = mul2(mu, make_float2(sc.up, sc.up));
-        z[i][0] = fmaf(mu.x, o[i][0], z[i][0]);
-        z[i][1] = fmaf(mu.y, o[i][1], z[i][1]);
-        z[i][2] = fmaf(mu.x, o[i][2], z[i][2]);
-        z[i][3] = fmaf(mu.y, o[i][3], z[i][3]);
+        const uint32_t o0 = movmatrix_trans(F16<T>::pack(p.scale * z[i][0], p.scale * z[i][1]));
+        const uint32_t o1 = movmatrix_trans(F16<T>::pack(p.scale * z[i][2], p.scale * z[i][3]));
+        const int64_t t = c * CH + 8 * i + gr;
+        if (t < len) {
+          *reinterpret_cast<uint32_t*>(out + t * p.out_ld) = o0;
+          *reinterpret_cast<uint32_t*>(out + t * p.out_ld + 8) = o1;
+        }
       }
     }
+    if (c >= n_runs) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[c % NST]);
+    if constexpr (kScaled<T>) scale_all(S, sc.up);
+    float state[D / 2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t o0 = movmatrix_trans(F16<T>::pack(p.scale * z[i][0], p.scale * z[i][1]));
-      const uint32_t o1 = movmatrix_trans(F16<T>::pack(p.scale * z[i][2], p.scale * z[i][3]));
-      const int64_t t = c * CH + 8 * i + gr;
-      if (t < len) {
-        *reinterpret_cast<uint32_t*>(out + t * p.out_ld) = o0;
-        *reinterpret_cast<uint32_t*>(out + t * p.out_ld + 8) = o1;
-      }
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) state[4 * j + e] = S[j][e];
+    step_tokens<T, D>(p, state, h, half * ROWS + warp * 16 + gr, seq, c * CH, min(CH, len - c * CH), lane);
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[j][e] = state[4 * j + e];
+    if constexpr (kScaled<T>) {
+      norm = root * warp_largest(S);
+      sc = Scale(norm);
+      scale_all(S, sc.down);
     }
+    ++c;
   }
   if constexpr (kScaled<T>) scale_all(S, sc.up);
 #pragma unroll

@@ -83,3 +83,84 @@ def test_gdn_queries_of_any_size(K, dt, power):  # noqa: F811
     err, row = np.abs(f64(out) - o), np.sqrt((o * o).mean(-1, keepdims=True))
     half = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[dt]
     assert (err <= half * np.abs(o) + 2.0 ** -14 * row + 2.0 ** -25).all(), f"{(err / row).max():.2e}"
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16])
+@pytest.mark.parametrize("T", [16, 17, 90])
+@pytest.mark.parametrize("size,value,g", [(0.3, 0, -0.7), (0.3, 0, -1.0), (1.0, 0, -3.0), (1e4, 1, -0.7), (1e4, 1, -2.0),
+                                          (1e4, 0, -1.0), (2.0 ** 60, 1, -1.0), (2.0 ** 60, 0, -0.7), (2.0 ** 60, 1, -3.0)])
+def test_gdn_states_that_decay_below_what_the_first_tokens_met(K, dt, T, size, value, g):  # noqa: F811
+    """Strong decay of a state that is far above the values (0: padding that writes nothing): finite, and
+    within the bounds of what the run began with."""
+    q, k, v, gb, S = make_gdn(1, T, 2, 4, 128, dt, seed=16, sigma=size)
+    v = v * value
+    gb[:, 0] = g
+    out, S1 = run_gdn(K, q, k, v, gb, S)
+    check_gdn(out, S1, q, k, v, gb, S, [T])
+
+
+def check_decaying(out, S1, q, k, v, gb, S0):
+    """As check_gdn, but what a token adds to the state's error is in proportion to the state that it meets, its
+    value and its update, and decays with the state: B_t = c_t B_(t-1) + e^g |S| + |v| + |u| with c_t the factor by
+    which the recurrence enlarges a difference, e^g max(1, |1 - beta |k|^2|); the state is off by at most
+    8 (2^-21 + 2^-20) 4 B in the Frobenius norm, a readout by half a step (fp16: of 2^-24 at least) and |q| times
+    that.  One sequence."""
+    eps = 8 * (2.0 ** -21 + 2.0 ** -20) * 4
+    u = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[q.dtype]
+    q, k, v, gb, S = f64(q)[0], f64(k)[0], f64(v)[0], f64(gb)[0], f64(S0)[0].copy()
+    T, nk, d = q.shape
+    nv = v.shape[1]
+    kh = np.arange(nv) // (nv // nk)
+    got, B, o = f64(out)[0], np.zeros(nv), np.zeros((nv, d))
+    for t in range(T):
+        dec, beta, kt, qt = np.exp(gb[0, :, t]), gb[1, :, t], k[t, kh], q[t, kh]
+        S = dec[:, None, None] * S
+        ut = beta[:, None] * (v[t] - np.einsum("hij,hj->hi", S, kt))
+        k2 = (kt * kt).sum(1)
+        B = dec * np.maximum(1, np.abs(1 - beta * k2)) * B + np.sqrt((S * S).sum((1, 2)))
+        B += np.sqrt((v[t] ** 2).sum(1)) + np.sqrt((ut ** 2).sum(1))
+        S = S + ut[:, :, None] * kt[:, None, :]
+        o = np.einsum("hij,hj->hi", S, qt)
+        lim = u * np.abs(o) + 2.0 ** -25 + ((1 + u) * eps * B * np.sqrt((qt * qt).sum(1)))[:, None]
+        err = np.abs(got[t] - o)
+        assert (err <= lim).all(), f"token {t}: {np.nanmax(err / lim):.2f} of the bound"
+    es = np.sqrt(((f64(S1)[0] - S) ** 2).sum((1, 2)))
+    # (a state that decays out of fp32's normal range, 2^-126 for each of 128 x 128 entries, has fewer bits or none)
+    lim = eps * B + 128 * 2.0 ** -126
+    assert (es <= lim).all(), f"state: {np.max(es / lim):.2e} of the bound"
+
+
+@pytest.mark.parametrize("T", [16, 17, 90])
+@pytest.mark.parametrize("dt,size,value", [(torch.bfloat16, 1.0, 0), (torch.bfloat16, 1.0, 1), (torch.bfloat16, 1e4, 0),
+                                           (torch.bfloat16, 1e4, 1), (torch.bfloat16, 2.0 ** 60, 1)])
+@pytest.mark.parametrize("g", [-0.3, -0.7, -1.0, -3.0])
+def test_gdn_the_states_own_size_sets_its_precision(K, T, dt, size, value, g):  # noqa: F811
+    """A state that decays from far above the values to their size, or to nothing where they are 0."""
+    q, k, v, gb, S = make_gdn(1, T, 2, 4, 128, dt, seed=17, sigma=size)
+    v = v * value
+    gb[:, 0] = g
+    out, S1 = run_gdn(K, q, k, v, gb, S)
+    check_decaying(out, S1, q, k, v, gb, S)
+
+
+@pytest.mark.parametrize("T", [7, 40, 90])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("what", ["growth", "beta", "keys", "late decay"])
+def test_gdn_gates_and_keys_beyond_their_range(K, T, dt, what):  # noqa: F811
+    """g above 0, beta up to 2 and below 0, keys of norm 2, a decay to nothing behind tokens without any: some
+    tokens of them, in some heads."""
+    q, k, v, gb, S = make_gdn(1, T, 2, 6, 128, dt, seed=18, g_scale=0.2)
+    k = k.clone()
+    if what == "growth":
+        gb[:, 0, ::2, T // 3:T // 3 + 6] = 0.7
+    elif what == "beta":
+        gb[:, 1, 1] *= 2
+        gb[:, 1, 4, ::5] *= -1
+    elif what == "keys":
+        k[:, T // 2:T // 2 + 3] *= 2
+    else:
+        v[:, T // 4:T // 4 + 24] = 0
+        gb[:, 0, ::2, T // 4:] = 0
+        gb[:, 0, ::2, T // 4 + 2] = -float("inf")
+    out, S1 = run_gdn(K, q, k, v, gb, S)
+    check_decaying(out, S1, q, k, v, gb, S)
