@@ -766,7 +766,8 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
         // the run's units, from its values and the state's rows as its tokens meet them
         up = sc.up;
         const Scale now(fmaxf(gv.y, gv.z * norm));
-        decay *= sc.up * now.down;
+        // (S times it stays below 18 x 2^8, but the units alone may be 2^200 apart, with nothing left of S)
+        decay = fminf(decay * sc.up * now.down, 1.7e38f);
         sc = now;
         // S <- e^g S (I - beta k k^T) + beta v k^T, 16 times
         norm = fmaf(16.25f, gv.y, gv.x * norm);

@@ -164,3 +164,24 @@ def test_gdn_gates_and_keys_beyond_their_range(K, T, dt, what):  # noqa: F811
         gb[:, 0, ::2, T // 4 + 2] = -float("inf")
     out, S1 = run_gdn(K, q, k, v, gb, S)
     check_decaying(out, S1, q, k, v, gb, S)
+
+
+@pytest.mark.parametrize("T", [16, 17, 40])
+@pytest.mark.parametrize("dt,size", [(torch.bfloat16, 1.0), (torch.bfloat16, 2.0 ** 60), (torch.bfloat16, 2.0 ** 90)])
+def test_gdn_a_state_that_is_wiped_out(K, T, dt, size):  # noqa: F811
+    """A decay to nothing at the first token and values of 0, then (from token 16 on) values far below the state
+    that was; and values that drop from far above to far below 1 with nothing written."""
+    q, k, v, gb, S = make_gdn(1, T, 2, 4, 128, dt, seed=19, sigma=size)
+    v = v / size
+    v[:, :16] = 0
+    gb[:, 0, :, 0] = -float("inf")
+    out, S1 = run_gdn(K, q, k, v, gb, S)
+    assert torch.isfinite(S1).all() and (out[:, :16] == 0).all()
+    check_decaying(out, S1, q, k, v, gb, S)
+    v = torch.cat((v[:, 16:] * 0 + size, v[:, 16:] * 0 + 1 / size), 1)[:, :T]
+    T = v.shape[1]
+    if T > 8:
+        q, k, gb = q[:, :T], k[:, :T], gb[..., :T].contiguous()
+        gb[:, 1], S[:] = 0, 0
+        out, S1 = run_gdn(K, q, k, v, gb, S)
+        assert (S1 == 0).all() and (out == 0).all()
