@@ -4,6 +4,7 @@
 // Row v of S takes only v_t[v], k_t and the gates, so the d rows of a head are
 // independent; the tokens are sequential.
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/kva_ops.h"
 #include "kva_common.cuh"
@@ -184,9 +185,10 @@ __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constan
 // The state may not see a 16-bit rounding (it carries over thousands of tokens), so S, W, Tm and the
 // updates enter as two fp16 terms: two products where the partner is K or Q, three where it has two terms
 // itself.  So do S and M on the way to the readout, which sees one 16-bit rounding only, the output's.  That
-// makes 110 MMAs a warp and run.  bf16 inputs take fp16 terms as well, in units that
-// follow the data: two bf16 terms left states 3.4e-6 off after 1024 tokens (fp16 terms: 2e-7), three of
-// them would cost 30 % of the time, the units cost 4 to 9 %.
+// makes 110 MMAs a warp and run.  The terms are in units that follow the data, or small states and values would
+// lose fp16's last bits (1e-3 of a state of 1e-4) and large ones leave its range; bf16 inputs take fp16 terms as
+// well: two bf16 terms left states 3.4e-6 off after 1024 tokens (fp16 terms: 2e-7), three of them would cost
+// 30 % of the time.
 //
 // What bounds it: a run's chain of dependent steps.  16/48 heads of 128, one sequence of 1024
 // tokens (96 blocks, one chain warp a scheduler): fp16 66 us, 1.03 us a run, of which Y and Z 945 cycles, W
@@ -219,8 +221,9 @@ struct Stage {
   static constexpr int DEC = EG + CH * 4;          // e^(gam_last - gam)[16]
   static constexpr int EZ = DEC + CH * 4;          // e^gam[16] in q's units
   static constexpr int MU = EZ + CH * 4;           // the units of M's rows
-  static constexpr int GL = MU + CH * 4;          // e^gam_last, (bf16) largest |v| and e^gam_t; 1: ordinary run
-  static constexpr int BYTES = GL + 128;
+  static constexpr int GL = MU + CH * 4;          // e^gam_last, e^gam_first; 1: ordinary run
+  static constexpr int VM = GL + 64;               // the largest |v| of each column; NaN if it has one
+  static constexpr int BYTES = VM + (ROWS * 2 + 127) / 128 * 128 + 64;
 };
 struct Prep {                                      // per preparing warp: L in fp32 (row stride 20), beta
   static constexpr int LDL = 20;
@@ -254,50 +257,51 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   hi = pack_f16(h.x, h.y);
   lo = pack_f16(l.x, l.y);
 }
-// bf16 inputs: the chain's products are fp16 as well, in units of a power of two that follows the data.
-// What is at most m is below 2^8 in its units.  m is the largest of a run's |v| and of the decayed norms
-// e^gam_t |S row| in which its tokens meet the state (the state at the run's end may be far below those);
-// with keys of norm <= 1 and beta <= 1, W, U and S of the run stay below 18 m: below fp16's 65504, and what
-// fp16 drops is 2^-32 m.  A run that ends far below m (strong decay of a state with little written to it)
-// would lose its own precision by that, and gates or keys out of their range could pass 18 m: such runs go
-// token by token in fp32 (step_tokens).
-constexpr float kFar = 256.f;        // m over the larger of |v| and the state's norm behind the run: 2^-24 of those
+// The chain's products take fp16 terms whatever the inputs' type, each state row's in units of a power of two
+// that follows its data.  What is at most m is below 2^8 in its units.  m is the largest of the row's |v| of a
+// run and of the decayed norms e^gam_t |S row| in which the run's tokens meet it (the row at the run's end may be
+// far below those); with keys of norm <= 1 and beta <= 1, W, U and S of the run stay below 18 m: below fp16's
+// 65504, and what fp16 drops is 2^-32 m.  A run that ends far below m (strong decay of a state with little
+// written to it) would lose its own precision by that, gates or keys out of their range could pass 18 m, and a
+// value that is not finite would reach the run's tokens before it: such runs go token by token in fp32
+// (step_tokens).
+constexpr float kFar = 256.f;        // m over the larger of |v| and the row's norm behind the run: 2^-24 of those
 constexpr float kKeyNorm2 = 1.015625f;  // keys of norm 1, each entry rounded to bf16
+constexpr float kMost = 1.7e38f;
 template <typename T>
-constexpr bool kScaled = F16<T>::umma_fmt == 1;
+constexpr bool kBf16 = F16<T>::umma_fmt == 1;
 struct Scale {
   float up, down;
   __device__ __forceinline__ explicit Scale(float m) {
-    const int e = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 7, -100), 100);
-    up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    const uint32_t e = max(__float_as_uint(m) & 0x7f800000u, 8u << 23) - (7u << 23);  // the exponent, at least -126
+    up = __uint_as_float(e);
+    down = __uint_as_float((254u << 23) - e);
   }
 };
-constexpr float kNoScale = 1e30f;  // NaN and what is from here on set no scale (their rows are lost, the others not)
-// the warp's largest |x|
+// the largest |x| of a lane's two rows (those of its fragments' lower and upper half)
 template <int N>
-__device__ __forceinline__ float warp_largest(const float (&x)[N][4]) {
-  float m = 0.f;
+__device__ __forceinline__ float2 largest_of_rows(const float (&x)[N][4]) {
+  float2 m = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < N; ++i)
+  for (int i = 0; i < N; ++i) {
+    m.x = fmaxf(m.x, fmaxf(fabsf(x[i][0]), fabsf(x[i][1])));
+    m.y = fmaxf(m.y, fmaxf(fabsf(x[i][2]), fabsf(x[i][3])));
+  }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(x[i][j]));
-  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-  if (m < kNoScale) return m;
-  m = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(x[i][j]) < kNoScale ? fabsf(x[i][j]) : 0.f);
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  for (int o = 1; o < 4; o <<= 1) {
+    m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
+    m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
+  }
+  return m;
 }
 template <int N>
-__device__ __forceinline__ void scale_all(float (&x)[N][4], float f) {
+__device__ __forceinline__ void scale_all(float (&x)[N][4], float2 f) {  // f: the factors of a lane's two rows
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
-      const float2 y = mul2(make_float2(x[i][j], x[i][j + 1]), make_float2(f, f));
+      const float y01 = j ? f.y : f.x;
+      const float2 y = mul2(make_float2(x[i][j], x[i][j + 1]), make_float2(y01, y01));
       x[i][j] = y.x;
       x[i][j + 1] = y.y;
     }
@@ -459,7 +463,7 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
       reinterpret_cast<float*>(st + St::EG)[lane] = expf(gam + gaml);
       reinterpret_cast<float*>(st + St::DEC)[lane] = expf((last - gam) + (lastl - gaml));
       Ls[CH * Prep::LDL + lane] = bt;
-      if (lane == 0) *reinterpret_cast<float*>(st + St::GL) = expf(last + lastl);
+      if (lane == 0) *reinterpret_cast<float2*>(st + St::GL) = make_float2(expf(last + lastl), expf(gam));
     }
     // pair decays of this thread's fragment elements (t = gr + 8 a, s = 8 i + 2 cq + e); the fast
     // exponential is off by 2^-22 + |x| 2^-24, and what is far has no weight
@@ -492,7 +496,24 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
     {
       const float k0 = gr & 1 ? kk[0][1] : kk[0][0], k1 = gr & 1 ? kk[1][3] : kk[1][2];  // |k_t|^2, t = gr, gr + 8
       ordinary = __all_sync(0xffffffffu, ordinary && (cq != gr >> 1 || (k0 <= kKeyNorm2 && k1 <= kKeyNorm2)));
-      if (lane == 0) reinterpret_cast<float*>(st + St::GL)[3] = ordinary ? 1.f : 0.f;
+      if (lane == 0) reinterpret_cast<float*>(st + St::GL)[2] = ordinary ? 1.f : 0.f;
+    }
+    {
+      // V's columns: a lane's piece of every RV-th row, then its like among the lanes
+      using V2 = std::conditional_t<kBf16<T>, __nv_bfloat162, __half2>;
+      uint4 big = make_uint4(0, 0, 0, 0);
+      V2* b2 = reinterpret_cast<V2*>(&big);
+#pragma unroll
+      for (int i = 0; i < CH / RV; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(st + St::V + piece<2 * ROWS>(i * RV + rv, xv));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b2[j] = __hmax2_nan(b2[j], __habs2(reinterpret_cast<const V2*>(&x)[j]));
+      }
+#pragma unroll
+      for (int o = PV; o < 32; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b2[j] = __hmax2_nan(b2[j], __shfl_xor_sync(0xffffffffu, b2[j], o));
+      if (rv == 0) reinterpret_cast<uint4*>(st + St::VM)[xv] = big;
     }
     // M, and the units of its rows: bf16, those of the query, whose row the chain's products take in fp16 too;
     // fp16, from M's own largest entry
@@ -506,7 +527,7 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
         mm[i][2 + e] = s <= gr + 8 ? pd[i][2 + e] * qk[i][2 + e] : 0.f;
       }
     float ez = expf(gam + gaml), m0, m1;  // the factors that take M's rows to their units
-    if constexpr (kScaled<T>) {
+    if constexpr (kBf16<T>) {
       __syncwarp();
       const Scale sq = rows_to_f16<D>(st + St::Q, lane);
       m0 = __shfl_sync(0xffffffffu, sq.down, 2 * gr);
@@ -590,31 +611,7 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
         *reinterpret_cast<uint4*>(st + St::TL + piece16(lane, i)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
-    if constexpr (kScaled<T>) {
-      // the largest |v| (as bf16 pairs; NaN falls out, and with a value near infinity it is looked up again)
-      __nv_bfloat162 pair = __float2bfloat162_rn(0.f);
-#pragma unroll
-      for (int i = 0; i < CH * ROWS / 256; ++i) {
-        const uint4 x = reinterpret_cast<const uint4*>(st + St::V)[32 * i + lane];
-        const __nv_bfloat162* v2 = reinterpret_cast<const __nv_bfloat162*>(&x);
-        pair = __hmax2(pair, __hmax2(__hmax2(__habs2(v2[0]), __habs2(v2[1])), __hmax2(__habs2(v2[2]), __habs2(v2[3]))));
-      }
-      float big = fmaxf(__low2float(pair), __high2float(pair));
-      big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-      if (big >= kNoScale) {
-        big = 0.f;
-        for (int i = lane; i < CH * ROWS; i += 32) {
-          const float f = fabsf(F16<T>::to(reinterpret_cast<const T*>(st + St::V)[i]));
-          if (f < kNoScale) big = fmaxf(big, f);
-        }
-        big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-      }
-      float decay = lane < CH ? reinterpret_cast<const float*>(st + St::EG)[lane] : 0.f;  // (NaN counts as the largest)
-      decay = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(decay)));
-      if (lane == 0) {
-        reinterpret_cast<float*>(st + St::GL)[1] = big;
-        reinterpret_cast<float*>(st + St::GL)[2] = decay;
-      }
+    if constexpr (kBf16<T>) {
       // the chain's products take K in fp16: exact but for what is below 2^-17
 #pragma unroll 2
       for (int i = lane; i < CH * D / 8; i += 32) {
@@ -658,7 +655,7 @@ __device__ __noinline__ void step_tokens(const GdnFwd& p, float* state, int h, i
     float2 a0 = make_float2(0.f, 0.f), a1 = a0;
 #pragma unroll
     for (int j = 0; j < D / 8; ++j) kk[j] = *reinterpret_cast<const uint32_t*>(k + 8 * j);
-    scale_all(S, dec);
+    scale_all(S, make_float2(dec, dec));
 #pragma unroll
     for (int j = 0; j < D / 8; ++j) {
       const float2 f = F16<T>::unpack(kk[j]);
@@ -717,15 +714,18 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
     S[j][3] = c.y;
   }
   T* out = static_cast<T*>(p.out) + seq * p.out_seq + h * D + half * ROWS + warp * 16 + 2 * cq;
-  // bf16: S is held in units of `sc.up`; `norm` bounds the norm of its rows
+  // S is held in units of `up`; `norm` bounds the norm of a row.  (Of the lane's two rows.)
   const float root = D == 128 ? 11.32f : 8.f;  // sqrt(D): a row's norm is at most that times its largest entry
-  float norm = 0.f;
-  Scale sc(1.f);
-  if constexpr (kScaled<T>) {
-    norm = root * warp_largest(S);
-    sc = Scale(n_runs ? norm : 128.f);  // (units of 1 without tokens: the state goes out as it came)
-    scale_all(S, sc.down);
-  }
+  float2 norm, up;
+  auto measure = [&]() {  // S in true size
+    const float2 m = largest_of_rows(S);
+    norm = make_float2(fminf(root * m.x, kMost), fminf(root * m.y, kMost));
+    const Scale s0(norm.x), s1(norm.y);
+    up = make_float2(s0.up, s1.up);
+    scale_all(S, make_float2(s0.down, s1.down));
+  };
+  if (n_runs) measure();
+  else norm = up = make_float2(1.f, 1.f);  // (no tokens: the state goes out as it came)
 
   int c = 0;
   while (true) {
@@ -738,10 +738,8 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
       const uint8_t* st = sm + (c % NST) * St::BYTES;
       const uint32_t sst = base + (c % NST) * St::BYTES;
       const float4 gv = *reinterpret_cast<const float4*>(st + St::GL);
-      // (the same for the whole warp)
-      if (gv.w == 0.f || (kScaled<T> && gv.z * norm > kFar * fmaxf(gv.y, gv.x * norm))) break;
-      // Y = S K^T, Z = S Q^T, both terms of S (the second's products apart: shorter chains)
-      float y[2][4] = {}, yl[2][4] = {}, z[2][4] = {}, zl[2][4] = {};
+      // Y = S K^T, Z = S Q^T, both terms of S
+      float y[2][4] = {}, yl[2][4] = {}, z[2][4] = {};
       uint32_t kf[2][4], qf[2][4];
       ldmatrix_x4(kf[0], sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, mi >> 1));
       ldmatrix_x4(qf[0], sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, mi >> 1));
@@ -756,42 +754,44 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
         mma2(y[0], y[1], ah, kf[ks & 1], 0, 2, 1, 3);
         mma2(yl[0], yl[1], al, kf[ks & 1], 0, 2, 1, 3);
         mma2(z[0], z[1], ah, qf[ks & 1], 0, 2, 1, 3);
-        mma2(zl[0], zl[1], al, qf[ks & 1], 0, 2, 1, 3);
+        mma2(z[0], z[1], al, qf[ks & 1], 0, 2, 1, 3);
       }
+      // Units for the run, from its values and the state's rows as its tokens meet them.  (The test comes after
+      // the products, which hide what it waits for: before them 421 against 406 us for 8 sequences.)
+      const T* vm = reinterpret_cast<const T*>(st + St::VM) + warp * 16 + gr;
+      const float2 mv = make_float2(F16<T>::to(vm[0]), F16<T>::to(vm[8]));
+      const float2 met = make_float2(gv.y * norm.x, gv.y * norm.y), left = make_float2(gv.x * norm.x, gv.x * norm.y);
+      const bool fits = gv.z != 0.f && mv.x <= kMost && mv.y <= kMost && met.x <= kFar * fmaxf(mv.x, left.x) &&
+                        met.y <= kFar * fmaxf(mv.y, left.y);
+      if (!__all_sync(0xffffffffu, fits)) break;
       // W = V^T - Y diag(e^gam)
       uint32_t vf[4], wh[4], wl[4];
       ldmatrix_x4_trans(vf, sst + St::V + piece<2 * ROWS>((mi >> 1) * 8 + lr, 2 * warp + (mi & 1)));
-      float decay = gv.x, up = 1.f;  // of S into the next run; the units of Y and Z
-      if constexpr (kScaled<T>) {
-        // the run's units, from its values and the state's rows as its tokens meet them
-        up = sc.up;
-        const Scale now(fmaxf(gv.y, gv.z * norm));
-        // (S times it stays below 18 x 2^8, but the units alone may be 2^200 apart, with nothing left of S)
-        decay = fminf(decay * sc.up * now.down, 1.7e38f);
-        sc = now;
-        // S <- e^g S (I - beta k k^T) + beta v k^T, 16 times
-        norm = fmaf(16.25f, gv.y, gv.x * norm);
-      }
+      const Scale now0(fmaxf(mv.x, met.x)), now1(fmaxf(mv.y, met.y));
+      // S into the run's units: what stays is below 18 x 2^8, but the units alone may be 2^250 apart, with nothing
+      // left of S
+      const float2 decay = make_float2(fminf(gv.x * up.x * now0.down, kMost), fminf(gv.x * up.y * now1.down, kMost));
+      // S <- e^g S (I - beta k k^T) + beta v k^T, 16 times
+      norm = make_float2(fminf(fmaf(16.25f, mv.x, left.x), kMost), fminf(fmaf(16.25f, mv.y, left.y), kMost));
       float w[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float2 e = *reinterpret_cast<const float2*>(st + St::EG + (8 * i + 2 * cq) * 4);
-        float2 ez = *reinterpret_cast<const float2*>(st + St::EZ + (8 * i + 2 * cq) * 4);
-        if constexpr (kScaled<T>) {
-          e = mul2(e, make_float2(up, up));
-          ez = mul2(ez, make_float2(up, up));
-        }
+        const float2 e = *reinterpret_cast<const float2*>(st + St::EG + (8 * i + 2 * cq) * 4);
+        const float2 ez = *reinterpret_cast<const float2*>(st + St::EZ + (8 * i + 2 * cq) * 4);
+        const float2 e0 = mul2(e, make_float2(up.x, up.x)), e1 = mul2(e, make_float2(up.y, up.y));
+        const float2 z0 = mul2(ez, make_float2(up.x, up.x)), z1 = mul2(ez, make_float2(up.y, up.y));
         const float2 v0 = F16<T>::unpack(vf[2 * i]), v1 = F16<T>::unpack(vf[2 * i + 1]);
-        w[i][0] = v0.x - e.x * (y[i][0] + yl[i][0]);
-        w[i][1] = v0.y - e.y * (y[i][1] + yl[i][1]);
-        w[i][2] = v1.x - e.x * (y[i][2] + yl[i][2]);
-        w[i][3] = v1.y - e.y * (y[i][3] + yl[i][3]);
-        z[i][0] = ez.x * (z[i][0] + zl[i][0]);
-        z[i][1] = ez.y * (z[i][1] + zl[i][1]);
-        z[i][2] = ez.x * (z[i][2] + zl[i][2]);
-        z[i][3] = ez.y * (z[i][3] + zl[i][3]);
+        w[i][0] = v0.x - e0.x * (y[i][0] + yl[i][0]);
+        w[i][1] = v0.y - e0.y * (y[i][1] + yl[i][1]);
+        w[i][2] = v1.x - e1.x * (y[i][2] + yl[i][2]);
+        w[i][3] = v1.y - e1.y * (y[i][3] + yl[i][3]);
+        z[i][0] *= z0.x;
+        z[i][1] *= z0.y;
+        z[i][2] *= z1.x;
+        z[i][3] *= z1.y;
       }
-      if constexpr (kScaled<T>) scale_all(w, sc.down);
+      scale_all(w, make_float2(now0.down, now1.down));
+      up = make_float2(now0.up, now1.up);
       split_a(w[0], w[1], wh, wl);
       // U = W Tm^T
       float u[2][4] = {}, ul[2][4] = {};
@@ -828,7 +828,10 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
         mma2(S[2 * ks], S[2 * ks + 1], dh, kt, 0, 1, 2, 3);
         mma2(S[2 * ks], S[2 * ks + 1], dl, kt, 0, 1, 2, 3);
       }
-      if (kScaled<T> && (c & 7) == 7) norm = fminf(norm, root * sc.up * warp_largest(S));
+      if ((c & 7) == 7) {
+        const float2 m = largest_of_rows(S);
+        norm = make_float2(fminf(norm.x, root * up.x * m.x), fminf(norm.y, root * up.y * m.y));
+      }
       // O = Z diag(e^gam) + U M^T, written token-major
       {
         uint32_t mh[4], ml[4];
@@ -840,12 +843,12 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
         mma2(o[0], o[1], uh, ml, 0, 2, 1, 3);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float2 mu = *reinterpret_cast<const float2*>(st + St::MU + (8 * i + 2 * cq) * 4);
-          if constexpr (kScaled<T>) mu = mul2(mu, make_float2(sc.up, sc.up));
-          z[i][0] = fmaf(mu.x, o[i][0], z[i][0]);
-          z[i][1] = fmaf(mu.y, o[i][1], z[i][1]);
-          z[i][2] = fmaf(mu.x, o[i][2], z[i][2]);
-          z[i][3] = fmaf(mu.y, o[i][3], z[i][3]);
+          const float2 mu = *reinterpret_cast<const float2*>(st + St::MU + (8 * i + 2 * cq) * 4);
+          const float2 mu0 = mul2(mu, make_float2(up.x, up.x)), mu1 = mul2(mu, make_float2(up.y, up.y));
+          z[i][0] = fmaf(mu0.x, o[i][0], z[i][0]);
+          z[i][1] = fmaf(mu0.y, o[i][1], z[i][1]);
+          z[i][2] = fmaf(mu1.x, o[i][2], z[i][2]);
+          z[i][3] = fmaf(mu1.y, o[i][3], z[i][3]);
         }
       }
       __syncwarp();
@@ -864,7 +867,7 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
     if (c >= n_runs) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[c % NST]);
-    if constexpr (kScaled<T>) scale_all(S, sc.up);
+    scale_all(S, up);
     float state[D / 2];
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
@@ -875,14 +878,10 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
     for (int j = 0; j < D / 8; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) S[j][e] = state[4 * j + e];
-    if constexpr (kScaled<T>) {
-      norm = root * warp_largest(S);
-      sc = Scale(norm);
-      scale_all(S, sc.down);
-    }
+    measure();
     ++c;
   }
-  if constexpr (kScaled<T>) scale_all(S, sc.up);
+  scale_all(S, up);
 #pragma unroll
   for (int j = 0; j < D / 8; ++j) {
     *reinterpret_cast<float2*>(p.state_out + srow + 8 * j) = make_float2(S[j][0], S[j][1]);

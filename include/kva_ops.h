@@ -120,14 +120,14 @@ int kva_op_gdn_scan(const void* k, const void* v, const float* gb, float* state,
  *   o_t = scale * S_t q_t
  * v head h reads k and q head h / (n_v / n_k).  The state is held in fp32 throughout.
  * Up to 8 tokens run one after the other in fp32; longer sequences in runs of 16 on the tensor
- * cores, where fp32 operands enter as the sum of two fp16 values (an error of 2^-21 relative).  With
- * KVA_F16 the state and v - S k must then stay below 65504.  With KVA_BF16 the fp16 values are in units of
- * a power of two that follows the data, and what is below 2^-32 of the largest v of a run and of the state's
- * rows as its first token meets them is dropped: any state and v up to 1e30 work.  A run goes token by
- * token in fp32 too (right, but about 10 times slower) if a g of it is above 0, a beta outside 0..1 or a
- * key's norm above 1 by more than its rounding, or (KVA_BF16) if the state decays in it by more than 256
- * to below that and its values' size.  A NaN or an infinity in a token's q, k or gates can reach the
- * tokens of its run before it too; one in v only its own column.
+ * cores, where fp32 operands enter as the sum of two fp16 values (an error of 2^-21 relative), each row
+ * of the state's in units of a power of two that follows its data; what is below 2^-32 of the largest v that
+ * a run brings the row and of the row as the run's first token meets it is dropped.  A run goes token by
+ * token in fp32 too (right, but about 10 times slower) if a g of it is above 0, a beta outside 0..1, a key's
+ * norm above 1 by more than its rounding or a v not finite, or if a row of the state decays in it by more
+ * than 256 to below that and its values' size.  Any finite state and v work.  A NaN or an infinity in v
+ * reaches its own column from its token on; one in a token's q or k or in its gates can reach the tokens of
+ * its run before it too.
  */
 typedef struct kva_gdn_forward_args {
   int32_t dtype;          /* 16-bit format of q, k, v and out: KVA_BF16 or KVA_F16 */

@@ -99,7 +99,7 @@ def test_gdn_states_that_decay_below_what_the_first_tokens_met(K, dt, T, size, v
     check_gdn(out, S1, q, k, v, gb, S, [T])
 
 
-def check_decaying(out, S1, q, k, v, gb, S0):
+def check_decaying(out, S1, q, k, v, gb, S0, scale=1.0):
     """As check_gdn, but what a token adds to the state's error is in proportion to the state that it meets, its
     value and its update, and decays with the state: B_t = c_t B_(t-1) + e^g |S| + |v| + |u| with c_t the factor by
     which the recurrence enlarges a difference, e^g max(1, |1 - beta |k|^2|); the state is off by at most
@@ -120,8 +120,8 @@ def check_decaying(out, S1, q, k, v, gb, S0):
         B = dec * np.maximum(1, np.abs(1 - beta * k2)) * B + np.sqrt((S * S).sum((1, 2)))
         B += np.sqrt((v[t] ** 2).sum(1)) + np.sqrt((ut ** 2).sum(1))
         S = S + ut[:, :, None] * kt[:, None, :]
-        o = np.einsum("hij,hj->hi", S, qt)
-        lim = u * np.abs(o) + 2.0 ** -25 + ((1 + u) * eps * B * np.sqrt((qt * qt).sum(1)))[:, None]
+        o = scale * np.einsum("hij,hj->hi", S, qt)
+        lim = u * np.abs(o) + 2.0 ** -25 + (scale * (1 + u) * eps * B * np.sqrt((qt * qt).sum(1)))[:, None]
         err = np.abs(got[t] - o)
         assert (err <= lim).all(), f"token {t}: {np.nanmax(err / lim):.2f} of the bound"
     es = np.sqrt(((f64(S1)[0] - S) ** 2).sum((1, 2)))
@@ -131,8 +131,9 @@ def check_decaying(out, S1, q, k, v, gb, S0):
 
 
 @pytest.mark.parametrize("T", [16, 17, 90])
-@pytest.mark.parametrize("dt,size,value", [(torch.bfloat16, 1.0, 0), (torch.bfloat16, 1.0, 1), (torch.bfloat16, 1e4, 0),
-                                           (torch.bfloat16, 1e4, 1), (torch.bfloat16, 2.0 ** 60, 1)])
+@pytest.mark.parametrize("dt,size,value", [(torch.float16, 1.0, 0), (torch.float16, 1.0, 1), (torch.bfloat16, 1.0, 0),
+                                           (torch.bfloat16, 1.0, 1), (torch.bfloat16, 1e4, 0), (torch.bfloat16, 1e4, 1),
+                                           (torch.bfloat16, 2.0 ** 60, 1)])
 @pytest.mark.parametrize("g", [-0.3, -0.7, -1.0, -3.0])
 def test_gdn_the_states_own_size_sets_its_precision(K, T, dt, size, value, g):  # noqa: F811
     """A state that decays from far above the values to their size, or to nothing where they are 0."""
@@ -167,7 +168,8 @@ def test_gdn_gates_and_keys_beyond_their_range(K, T, dt, what):  # noqa: F811
 
 
 @pytest.mark.parametrize("T", [16, 17, 40])
-@pytest.mark.parametrize("dt,size", [(torch.bfloat16, 1.0), (torch.bfloat16, 2.0 ** 60), (torch.bfloat16, 2.0 ** 90)])
+@pytest.mark.parametrize("dt,size", [(torch.bfloat16, 1.0), (torch.bfloat16, 2.0 ** 60), (torch.bfloat16, 2.0 ** 90),
+                                     (torch.float16, 1.0), (torch.float16, 2.0 ** 12)])
 def test_gdn_a_state_that_is_wiped_out(K, T, dt, size):  # noqa: F811
     """A decay to nothing at the first token and values of 0, then (from token 16 on) values far below the state
     that was; and values that drop from far above to far below 1 with nothing written."""
@@ -185,3 +187,50 @@ def test_gdn_a_state_that_is_wiped_out(K, T, dt, size):  # noqa: F811
         gb[:, 1], S[:] = 0, 0
         out, S1 = run_gdn(K, q, k, v, gb, S)
         assert (S1 == 0).all() and (out == 0).all()
+
+
+@pytest.mark.parametrize("T", [8, 16, 80])
+@pytest.mark.parametrize("dt,state,value", [
+    (torch.float16, 1e-2, 1e-2), (torch.float16, 1e-3, 1e-3), (torch.float16, 1e-4, 1e-4), (torch.float16, 0, 1e-5),
+    (torch.float16, 1e-30, 1e-6), (torch.float16, 1e6, 1e4), (torch.float16, 1e30, 0), (torch.bfloat16, 0, 1e-30),
+    (torch.bfloat16, 1e-30, 1e-30), (torch.bfloat16, 1e30, 1e30), (torch.bfloat16, 1e34, 0)])
+def test_gdn_values_and_states_of_any_size(K, T, dt, state, value):  # noqa: F811
+    """fp32's precision relative to what the state and the values are, as token by token."""
+    q, k, v, gb, S = make_gdn(1, T, 2, 4, 128, dt, seed=20, sigma=state, g_scale=0.2)
+    v = (v.float() * value).to(dt)
+    scale = 1 / max(state, value, 1.0)
+    out, S1 = run_gdn(K, q, k, v, gb, S, scale=scale)
+    check_decaying(out, S1, q, k, v, gb, S, scale)
+
+
+@pytest.mark.parametrize("T", [8, 80])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+def test_gdn_a_row_of_the_state_depends_on_its_own_column_of_v_only(K, T, dt):  # noqa: F811
+    """An outlier column, and a NaN and an infinity in two others: everything else keeps every bit, those
+    columns' tokens before them too."""
+    q, k, v, gb, S = make_gdn(1, T, 2, 4, 128, dt, seed=21, g_scale=0.2)
+    out, S1 = run_gdn(K, q, k, v, gb, S)
+    v2, t = v.clone(), 5
+    v2[:, :, 1, 5] *= 2.0 ** 12
+    out2, S2 = run_gdn(K, q, k, v2, gb, S)
+    same = torch.ones(4, 128, dtype=torch.bool, device="cuda")
+    same[1, 5] = False
+    assert torch.equal(out2[0][:, same], out[0][:, same]) and torch.equal(S2[0][same], S1[0][same])
+    v2 = v.clone()
+    v2[0, t, 0, 17], v2[0, t, 3, 127] = float("nan"), float("inf")
+    out2, S2 = run_gdn(K, q, k, v2, gb, S)
+    lost = torch.zeros(4, 128, dtype=torch.bool, device="cuda")
+    lost[0, 17] = lost[3, 127] = True
+    assert not torch.isfinite(out2[0, t:][:, lost]).any() and not torch.isfinite(S2[0][lost]).any()
+    v3 = v2.clone()
+    v3[0, t, 0, 17], v3[0, t, 3, 127] = 0, 0
+    o, _, _, _, _ = gdn_plain(f64(q), f64(k), f64(v3), f64(gb), f64(S), [T], 1.0)
+    half = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[dt]
+    got, o = f64(out2[0, :t][:, lost]), o[0, :t][:, lost.cpu().numpy()]
+    assert (np.abs(got - o) <= (half + 2.0 ** -12) * np.abs(o).max() + 2.0 ** -20).all()
+    rest = ~lost
+    check = torch.where(rest, out2[0], out2.new_zeros(())), torch.where(rest[..., None], S2[0], S2.new_zeros(()))
+    v3[0, :, 0, 17], v3[0, :, 3, 127] = 0, 0
+    S3 = S.clone()
+    S3[0][lost] = 0
+    check_decaying(check[0][None], check[1][None], q, k, v3, gb, S3)
