@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constan
 // ============================================================================
 // Runs of 16 tokens on mma.sync.  With gam_t = sum_{s<=t} g_s inside a run and S the state at
 // its start,
-//     L[t,s] = beta_t e^(gam_t-gam_s) k_t.k_s (s < t),     Tm = (I + L)^-1 diag(beta),
-//     U      = (V^T - S K^T diag(e^gam)) Tm^T              (column s: the update u_s),
+//     L[t,s] = e^(gam_t-gam_s) k_t.k_s beta_s (s < t),     Tm = (I + L)^-1,
+//     U      = (V^T - S K^T diag(e^gam)) Tm^T diag(beta)   (column s: the update u_s),
 //     O      = S Q^T diag(e^gam) + U M^T,                  M[t,s] = e^(gam_t-gam_s) q_t.k_s (s <= t),
 //     S     <- e^gam_last S + U diag(e^(gam_last-gam)) K.
 // Tm, M and the decays take no state: preparing warps form them ahead of the chain.  A chain warp
@@ -213,7 +213,7 @@ struct Stage {
   static constexpr int K = 0;                      // [16][D], 16-byte pieces xor-swizzled by row
   static constexpr int Q = K + CH * D * 2;
   static constexpr int V = Q + CH * D * 2;         // [16][ROWS], this block's columns
-  static constexpr int TH = V + CH * ROWS * 2;     // Tm as two 16-bit terms, [s][t]
+  static constexpr int TH = V + CH * ROWS * 2;     // 2^10 Tm as two 16-bit terms, [s][t]
   static constexpr int TL = TH + CH * CH * 2;
   static constexpr int MH = TL + CH * CH * 2;      // M as two 16-bit terms in units of MU, [t][s]
   static constexpr int ML = MH + CH * CH * 2;
@@ -221,13 +221,14 @@ struct Stage {
   static constexpr int DEC = EG + CH * 4;          // e^(gam_last - gam)[16]
   static constexpr int EZ = DEC + CH * 4;          // e^gam[16] in q's units
   static constexpr int MU = EZ + CH * 4;           // the units of M's rows
-  static constexpr int GL = MU + CH * 4;          // e^gam_last, e^gam_first; 1: ordinary run
+  static constexpr int BT = MU + CH * 4;           // 2^-10 beta
+  static constexpr int GL = BT + CH * 4;          // e^gam_last, e^gam_first; 1: ordinary run; largest beta
   static constexpr int VM = GL + 64;               // the largest |v| of each column; NaN if it has one
-  static constexpr int BYTES = VM + (ROWS * 2 + 127) / 128 * 128 + 64;
+  static constexpr int BYTES = (VM + ROWS * 2 + 127) / 128 * 128;
 };
-struct Prep {                                      // per preparing warp: L in fp32 (row stride 20), beta
+struct Prep {                                      // per preparing warp: L in fp32 (row stride 20)
   static constexpr int LDL = 20;
-  static constexpr int BYTES = (CH * LDL + CH) * 4;
+  static constexpr int BYTES = CH * LDL * 4;
 };
 template <int D, int ROWS, int PREP>
 struct Chunk {
@@ -258,14 +259,15 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = pack_f16(l.x, l.y);
 }
 // The chain's products take fp16 terms whatever the inputs' type, each state row's in units of a power of two
-// that follows its data.  What is at most m is below 2^8 in its units.  m is the largest of the row's |v| of a
-// run and of the decayed norms e^gam_t |S row| in which the run's tokens meet it (the row at the run's end may be
-// far below those); with keys of norm <= 1 and beta <= 1, W, U and S of the run stay below 18 m: below fp16's
-// 65504, and what fp16 drops is 2^-32 m.  A run that ends far below m (strong decay of a state with little
+// that follows its data.  What is at most m is below 2^8 in its units.  For S and U, m is the largest of the
+// row's beta |v| of a run (as the product of both's largest) and of the decayed norms e^gam_t |S row| in which the
+// run's tokens meet it (the row at the run's end may be far below those); for W, of |v| and those.  With keys of
+// norm <= 1 and beta <= 1 all stay below 18 m: below fp16's 65504, and what fp16 drops is 2^-32 m (2^-35 of Tm,
+// whose entries are at most 1).  A run that ends far below m (strong decay of a state with little
 // written to it) would lose its own precision by that, gates or keys out of their range could pass 18 m, and a
 // value that is not finite would reach the run's tokens before it: such runs go token by token in fp32
 // (step_tokens).
-constexpr float kFar = 256.f;        // m over the larger of |v| and the row's norm behind the run: 2^-24 of those
+constexpr float kFar = 256.f;  // m over the larger of beta |v| and the row's norm behind the run: 2^-24 of those
 constexpr float kKeyNorm2 = 1.015625f;  // keys of norm 1, each entry rounded to bf16
 constexpr float kMost = 1.7e38f;
 template <typename T>
@@ -462,7 +464,7 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
     if (lane < CH) {
       reinterpret_cast<float*>(st + St::EG)[lane] = expf(gam + gaml);
       reinterpret_cast<float*>(st + St::DEC)[lane] = expf((last - gam) + (lastl - gaml));
-      Ls[CH * Prep::LDL + lane] = bt;
+      reinterpret_cast<float*>(st + St::BT)[lane] = bt * 0x1p-10f;
       if (lane == 0) *reinterpret_cast<float2*>(st + St::GL) = make_float2(expf(last + lastl), expf(gam));
     }
     // pair decays of this thread's fragment elements (t = gr + 8 a, s = 8 i + 2 cq + e); the fast
@@ -496,7 +498,8 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
     {
       const float k0 = gr & 1 ? kk[0][1] : kk[0][0], k1 = gr & 1 ? kk[1][3] : kk[1][2];  // |k_t|^2, t = gr, gr + 8
       ordinary = __all_sync(0xffffffffu, ordinary && (cq != gr >> 1 || (k0 <= kKeyNorm2 && k1 <= kKeyNorm2)));
-      if (lane == 0) reinterpret_cast<float*>(st + St::GL)[2] = ordinary ? 1.f : 0.f;
+      const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bt)));
+      if (lane == 0) reinterpret_cast<float2*>(st + St::GL)[1] = make_float2(ordinary ? 1.f : 0.f, most);
     }
     {
       // V's columns: a lane's piece of every RV-th row, then its like among the lanes
@@ -556,14 +559,14 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
       }
     }
     if (lane < CH) reinterpret_cast<float*>(st + St::EZ)[lane] = ez;
-    const float bt0 = __shfl_sync(0xffffffffu, bt, gr), bt1 = __shfl_sync(0xffffffffu, bt, gr + 8);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int s = 8 * i + 2 * cq;
+      const float b0 = __shfl_sync(0xffffffffu, bt, s), b1 = __shfl_sync(0xffffffffu, bt, s + 1);
       *reinterpret_cast<float2*>(Ls + gr * Prep::LDL + s) =
-          make_float2(s < gr ? bt0 * pd[i][0] * kk[i][0] : 0.f, s + 1 < gr ? bt0 * pd[i][1] * kk[i][1] : 0.f);
+          make_float2(s < gr ? b0 * pd[i][0] * kk[i][0] : 0.f, s + 1 < gr ? b1 * pd[i][1] * kk[i][1] : 0.f);
       *reinterpret_cast<float2*>(Ls + (gr + 8) * Prep::LDL + s) =
-          make_float2(s < gr + 8 ? bt1 * pd[i][2] * kk[i][2] : 0.f, s + 1 < gr + 8 ? bt1 * pd[i][3] * kk[i][3] : 0.f);
+          make_float2(s < gr + 8 ? b0 * pd[i][2] * kk[i][2] : 0.f, s + 1 < gr + 8 ? b1 * pd[i][3] * kk[i][3] : 0.f);
       uint32_t hi, lo;
       split2(mm[i][0] * m0, mm[i][1] * m0, hi, lo);
       *reinterpret_cast<uint32_t*>(st + St::MH + piece16(gr, i) + 4 * cq) = hi;
@@ -574,9 +577,9 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
     }
     __syncwarp();
     // (I + L)^-1 in fp32, row r = lane: x (I + L) = e_r from the last column down (x_s is final
-    // when reached and leaves every earlier column); times beta of the column
+    // when reached and leaves every earlier column)
     if (lane < CH) {
-      float x[CH], bb[CH];
+      float x[CH];
 #pragma unroll
       for (int s = 0; s < CH; ++s) x[s] = s == lane ? 1.f : 0.f;
 #pragma unroll
@@ -594,19 +597,11 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
         for (int i = 0; i < s; ++i) x[i] = fmaf(-x[s], l[i], x[i]);
       }
 #pragma unroll
-      for (int s = 0; s < CH; s += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(Ls + CH * Prep::LDL + s);
-        bb[s] = f.x;
-        bb[s + 1] = f.y;
-        bb[s + 2] = f.z;
-        bb[s + 3] = f.w;
-      }
-#pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          split2(x[8 * i + 2 * j] * bb[8 * i + 2 * j], x[8 * i + 2 * j + 1] * bb[8 * i + 2 * j + 1], hi[j], lo[j]);
+          split2(0x1p10f * x[8 * i + 2 * j], 0x1p10f * x[8 * i + 2 * j + 1], hi[j], lo[j]);
         *reinterpret_cast<uint4*>(st + St::TH + piece16(lane, i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(st + St::TL + piece16(lane, i)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
@@ -739,7 +734,7 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
       const uint32_t sst = base + (c % NST) * St::BYTES;
       const float4 gv = *reinterpret_cast<const float4*>(st + St::GL);
       // Y = S K^T, Z = S Q^T, both terms of S
-      float y[2][4] = {}, yl[2][4] = {}, z[2][4] = {};
+      float y[2][4] = {}, z[2][4] = {};
       uint32_t kf[2][4], qf[2][4];
       ldmatrix_x4(kf[0], sst + St::K + piece<2 * D>((mi & 1) * 8 + lr, mi >> 1));
       ldmatrix_x4(qf[0], sst + St::Q + piece<2 * D>((mi & 1) * 8 + lr, mi >> 1));
@@ -752,7 +747,7 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
         uint32_t ah[4], al[4];
         split_a(S[2 * ks], S[2 * ks + 1], ah, al);
         mma2(y[0], y[1], ah, kf[ks & 1], 0, 2, 1, 3);
-        mma2(yl[0], yl[1], al, kf[ks & 1], 0, 2, 1, 3);
+        mma2(y[0], y[1], al, kf[ks & 1], 0, 2, 1, 3);
         mma2(z[0], z[1], ah, qf[ks & 1], 0, 2, 1, 3);
         mma2(z[0], z[1], al, qf[ks & 1], 0, 2, 1, 3);
       }
@@ -760,19 +755,23 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
       // the products, which hide what it waits for: before them 421 against 406 us for 8 sequences.)
       const T* vm = reinterpret_cast<const T*>(st + St::VM) + warp * 16 + gr;
       const float2 mv = make_float2(F16<T>::to(vm[0]), F16<T>::to(vm[8]));
+      const float most = fmaxf(gv.w, 0x1p-100f);  // (a smaller beta is written with fewer bits)
+      const float2 bm = make_float2(most * mv.x, most * mv.y);
       const float2 met = make_float2(gv.y * norm.x, gv.y * norm.y), left = make_float2(gv.x * norm.x, gv.x * norm.y);
-      const bool fits = gv.z != 0.f && mv.x <= kMost && mv.y <= kMost && met.x <= kFar * fmaxf(mv.x, left.x) &&
-                        met.y <= kFar * fmaxf(mv.y, left.y);
+      const bool fits = gv.z != 0.f && mv.x <= kMost && mv.y <= kMost && met.x <= kFar * fmaxf(bm.x, left.x) &&
+                        met.y <= kFar * fmaxf(bm.y, left.y);
       if (!__all_sync(0xffffffffu, fits)) break;
       // W = V^T - Y diag(e^gam)
       uint32_t vf[4], wh[4], wl[4];
       ldmatrix_x4_trans(vf, sst + St::V + piece<2 * ROWS>((mi >> 1) * 8 + lr, 2 * warp + (mi & 1)));
-      const Scale now0(fmaxf(mv.x, met.x)), now1(fmaxf(mv.y, met.y));
+      const Scale now0(fmaxf(bm.x, met.x)), now1(fmaxf(bm.y, met.y));  // of S and U
+      const Scale w0(fmaxf(mv.x, met.x)), w1(fmaxf(mv.y, met.y));      // of W
+      const float2 into = make_float2(w0.up * now0.down, w1.up * now1.down);  // from these to those, at most 2^101
       // S into the run's units: what stays is below 18 x 2^8, but the units alone may be 2^250 apart, with nothing
       // left of S
       const float2 decay = make_float2(fminf(gv.x * up.x * now0.down, kMost), fminf(gv.x * up.y * now1.down, kMost));
       // S <- e^g S (I - beta k k^T) + beta v k^T, 16 times
-      norm = make_float2(fminf(fmaf(16.25f, mv.x, left.x), kMost), fminf(fmaf(16.25f, mv.y, left.y), kMost));
+      norm = make_float2(fminf(fmaf(16.25f, bm.x, left.x), kMost), fminf(fmaf(16.25f, bm.y, left.y), kMost));
       float w[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -781,27 +780,27 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
         const float2 e0 = mul2(e, make_float2(up.x, up.x)), e1 = mul2(e, make_float2(up.y, up.y));
         const float2 z0 = mul2(ez, make_float2(up.x, up.x)), z1 = mul2(ez, make_float2(up.y, up.y));
         const float2 v0 = F16<T>::unpack(vf[2 * i]), v1 = F16<T>::unpack(vf[2 * i + 1]);
-        w[i][0] = v0.x - e0.x * (y[i][0] + yl[i][0]);
-        w[i][1] = v0.y - e0.y * (y[i][1] + yl[i][1]);
-        w[i][2] = v1.x - e1.x * (y[i][2] + yl[i][2]);
-        w[i][3] = v1.y - e1.y * (y[i][3] + yl[i][3]);
+        w[i][0] = v0.x - e0.x * y[i][0];
+        w[i][1] = v0.y - e0.y * y[i][1];
+        w[i][2] = v1.x - e1.x * y[i][2];
+        w[i][3] = v1.y - e1.y * y[i][3];
         z[i][0] *= z0.x;
         z[i][1] *= z0.y;
         z[i][2] *= z1.x;
         z[i][3] *= z1.y;
       }
-      scale_all(w, make_float2(now0.down, now1.down));
+      scale_all(w, make_float2(w0.down, w1.down));
       up = make_float2(now0.up, now1.up);
       split_a(w[0], w[1], wh, wl);
-      // U = W Tm^T
-      float u[2][4] = {}, ul[2][4] = {};
+      // U = W Tm^T diag(beta), from W's units to S's
+      float u[2][4] = {};
       {
         uint32_t th[4], tl[4];
         ldmatrix_x4(th, sst + St::TH + piece16((mi & 1) * 8 + lr, mi >> 1));
         ldmatrix_x4(tl, sst + St::TL + piece16((mi & 1) * 8 + lr, mi >> 1));
         mma2(u[0], u[1], wh, th, 0, 2, 1, 3);
-        mma2(ul[0], ul[1], wl, th, 0, 2, 1, 3);
-        mma2(ul[0], ul[1], wh, tl, 0, 2, 1, 3);
+        mma2(u[0], u[1], wl, th, 0, 2, 1, 3);
+        mma2(u[0], u[1], wh, tl, 0, 2, 1, 3);
       }
       uint32_t uh[4], uo[4], dh[4], dl[4];
       {
@@ -809,8 +808,12 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float2 e = *reinterpret_cast<const float2*>(st + St::DEC + (8 * i + 2 * cq) * 4);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) u[i][j] += ul[i][j];
+          const float2 b = *reinterpret_cast<const float2*>(st + St::BT + (8 * i + 2 * cq) * 4);
+          const float2 b0 = mul2(b, make_float2(into.x, into.x)), b1 = mul2(b, make_float2(into.y, into.y));
+          u[i][0] *= b0.x;
+          u[i][1] *= b0.y;
+          u[i][2] *= b1.x;
+          u[i][3] *= b1.y;
           dd[i][0] = u[i][0] * e.x;
           dd[i][1] = u[i][1] * e.y;
           dd[i][2] = u[i][2] * e.x;

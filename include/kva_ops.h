@@ -121,8 +121,8 @@ int kva_op_gdn_scan(const void* k, const void* v, const float* gb, float* state,
  * v head h reads k and q head h / (n_v / n_k).  The state is held in fp32 throughout.
  * Up to 8 tokens run one after the other in fp32; longer sequences in runs of 16 on the tensor
  * cores, where fp32 operands enter as the sum of two fp16 values (an error of 2^-21 relative), each row
- * of the state's in units of a power of two that follows its data; what is below 2^-32 of the largest v that
- * a run brings the row and of the row as the run's first token meets it is dropped.  A run goes token by
+ * of the state's in units of a power of two that follows its data; what is below 2^-32 of the largest beta v
+ * that a run brings the row and of the row as the run's first token meets it is dropped.  A run goes token by
  * token in fp32 too (right, but about 10 times slower) if a g of it is above 0, a beta outside 0..1, a key's
  * norm above 1 by more than its rounding or a v not finite, or if a row of the state decays in it by more
  * than 256 to below that and its values' size.  Any finite state and v work.  A NaN or an infinity in v

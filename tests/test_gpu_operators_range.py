@@ -100,8 +100,8 @@ def test_gdn_states_that_decay_below_what_the_first_tokens_met(K, dt, T, size, v
 
 
 def check_decaying(out, S1, q, k, v, gb, S0, scale=1.0):
-    """As check_gdn, but what a token adds to the state's error is in proportion to the state that it meets, its
-    value and its update, and decays with the state: B_t = c_t B_(t-1) + e^g |S| + |v| + |u| with c_t the factor by
+    """As check_gdn, but what a token adds to the state's error is in proportion to the state that it meets and its
+    update's parts, and decays with the state: B_t = c_t B_(t-1) + e^g |S| + |beta| |v| + |u| with c_t the factor by
     which the recurrence enlarges a difference, e^g max(1, |1 - beta |k|^2|); the state is off by at most
     8 (2^-21 + 2^-20) 4 B in the Frobenius norm, a readout by half a step (fp16: of 2^-24 at least) and |q| times
     that.  One sequence."""
@@ -118,7 +118,7 @@ def check_decaying(out, S1, q, k, v, gb, S0, scale=1.0):
         ut = beta[:, None] * (v[t] - np.einsum("hij,hj->hi", S, kt))
         k2 = (kt * kt).sum(1)
         B = dec * np.maximum(1, np.abs(1 - beta * k2)) * B + np.sqrt((S * S).sum((1, 2)))
-        B += np.sqrt((v[t] ** 2).sum(1)) + np.sqrt((ut ** 2).sum(1))
+        B += np.abs(beta) * np.sqrt((v[t] ** 2).sum(1)) + np.sqrt((ut ** 2).sum(1))
         S = S + ut[:, :, None] * kt[:, None, :]
         o = scale * np.einsum("hij,hj->hi", S, qt)
         lim = u * np.abs(o) + 2.0 ** -25 + (scale * (1 + u) * eps * B * np.sqrt((qt * qt).sum(1)))[:, None]
@@ -234,3 +234,18 @@ def test_gdn_a_row_of_the_state_depends_on_its_own_column_of_v_only(K, T, dt):  
     S3 = S.clone()
     S3[0][lost] = 0
     check_decaying(check[0][None], check[1][None], q, k, v3, gb, S3)
+
+
+@pytest.mark.parametrize("T", [8, 16, 90])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("state", [0, 1e-4, 1.0])
+@pytest.mark.parametrize("beta", [1e-2, 1e-4, 1e-6, 1e-12])
+def test_gdn_heads_that_write_little(K, T, dt, state, beta):  # noqa: F811
+    """beta far below 1, alone or beside a head that writes in full: fp32's precision of what is written."""
+    q, k, v, gb, S = make_gdn(1, T, 2, 4, 128, dt, seed=22, sigma=state, g_scale=0.2)
+    gb[:, 1, :3] *= beta
+    scale = 1.0 if state else 2.0 ** -10 / beta  # readouts in the output's range
+    out, S1 = run_gdn(K, q, k, v, gb, S, scale=scale)
+    for i in range(2 if state else 1):  # (with that scale the head that writes in full leaves the range)
+        h, kh = slice(2 * i, 2 * i + 2), slice(i, i + 1)
+        check_decaying(out[:, :, h], S1[:, h], q[:, :, kh], k[:, :, kh], v[:, :, h], gb[:, :, h], S[:, h], scale)
