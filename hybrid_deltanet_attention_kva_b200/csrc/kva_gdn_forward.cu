@@ -264,11 +264,12 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 // run's tokens meet it (the row at the run's end may be far below those); for W, of |v| and those.  With keys of
 // norm <= 1 and beta <= 1 all stay below 18 m: below fp16's 65504, and what fp16 drops is 2^-32 m (2^-35 of Tm,
 // whose entries are at most 1).  A run that ends far below m (strong decay of a state with little
-// written to it) would lose its own precision by that, gates or keys out of their range could pass 18 m, and a
-// value that is not finite would reach the run's tokens before it: such runs go token by token in fp32
-// (step_tokens).
+// written to it) would lose its own precision by that, and a tiny bf16 key its last bits in fp16; gates or
+// keys out of their range could pass 18 m, and a value that is not finite would reach the run's tokens before
+// it: such runs go token by token in fp32 (step_tokens).
 constexpr float kFar = 256.f;  // m over the larger of beta |v| and the row's norm behind the run: 2^-24 of those
 constexpr float kKeyNorm2 = 1.015625f;  // keys of norm 1, each entry rounded to bf16
+constexpr float kTinyKey2 = 0x1p-12f;   // bf16 keys of norm 2^-6: few entries below fp16's normal range
 constexpr float kMost = 1.7e38f;
 template <typename T>
 constexpr bool kBf16 = F16<T>::umma_fmt == 1;
@@ -497,7 +498,8 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
     }
     {
       const float k0 = gr & 1 ? kk[0][1] : kk[0][0], k1 = gr & 1 ? kk[1][3] : kk[1][2];  // |k_t|^2, t = gr, gr + 8
-      ordinary = __all_sync(0xffffffffu, ordinary && (cq != gr >> 1 || (k0 <= kKeyNorm2 && k1 <= kKeyNorm2)));
+      auto fits = [](float k2) { return k2 <= kKeyNorm2 && (!kBf16<T> || k2 >= kTinyKey2 || k2 == 0.f); };
+      ordinary = __all_sync(0xffffffffu, ordinary && (cq != gr >> 1 || (fits(k0) && fits(k1))));
       const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bt)));
       if (lane == 0) reinterpret_cast<float2*>(st + St::GL)[1] = make_float2(ordinary ? 1.f : 0.f, most);
     }
@@ -606,8 +608,7 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
         *reinterpret_cast<uint4*>(st + St::TL + piece16(lane, i)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
-    if constexpr (kBf16<T>) {
-      // the chain's products take K in fp16: exact but for what is below 2^-17
+    if constexpr (kBf16<T>) {  // the chain's products take K in fp16 too: exact but for what is below 2^-17
 #pragma unroll 2
       for (int i = lane; i < CH * D / 8; i += 32) {
         uint4* k8 = reinterpret_cast<uint4*>(st + St::K) + i;

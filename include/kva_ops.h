@@ -124,10 +124,10 @@ int kva_op_gdn_scan(const void* k, const void* v, const float* gb, float* state,
  * of the state's in units of a power of two that follows its data; what is below 2^-32 of the largest beta v
  * that a run brings the row and of the row as the run's first token meets it is dropped.  A run goes token by
  * token in fp32 too (right, but about 10 times slower) if a g of it is above 0, a beta outside 0..1, a key's
- * norm above 1 by more than its rounding or a v not finite, or if a row of the state decays in it by more
- * than 256 to below that and its values' size.  Any finite state and v work.  A NaN or an infinity in v
- * reaches its own column from its token on; one in a token's q or k or in its gates can reach the tokens of
- * its run before it too.
+ * norm above 1 by more than its rounding or (KVA_BF16) below 2^-6 but not 0, or a v not finite, or if a row of
+ * the state decays in it by more than 256 to below that and its values' size.  Any finite state and v work.
+ * A NaN or an infinity in v reaches its own column from its token on; one in a token's q or k or in its
+ * gates can reach the tokens of its run before it too.
  */
 typedef struct kva_gdn_forward_args {
   int32_t dtype;          /* 16-bit format of q, k, v and out: KVA_BF16 or KVA_F16 */

@@ -101,7 +101,7 @@ def test_gdn_states_that_decay_below_what_the_first_tokens_met(K, dt, T, size, v
 
 def check_decaying(out, S1, q, k, v, gb, S0, scale=1.0):
     """As check_gdn, but what a token adds to the state's error is in proportion to the state that it meets and its
-    update's parts, and decays with the state: B_t = c_t B_(t-1) + e^g |S| + |beta| |v| + |u| with c_t the factor by
+    update's parts, and decays with the state: B_t = c_t B_(t-1) + e^g |S| + (|beta| |v| + |u|) |k| with c_t the factor by
     which the recurrence enlarges a difference, e^g max(1, |1 - beta |k|^2|); the state is off by at most
     8 (2^-21 + 2^-20) 4 B in the Frobenius norm, a readout by half a step (fp16: of 2^-24 at least) and |q| times
     that.  One sequence."""
@@ -118,7 +118,7 @@ def check_decaying(out, S1, q, k, v, gb, S0, scale=1.0):
         ut = beta[:, None] * (v[t] - np.einsum("hij,hj->hi", S, kt))
         k2 = (kt * kt).sum(1)
         B = dec * np.maximum(1, np.abs(1 - beta * k2)) * B + np.sqrt((S * S).sum((1, 2)))
-        B += np.abs(beta) * np.sqrt((v[t] ** 2).sum(1)) + np.sqrt((ut ** 2).sum(1))
+        B += (np.abs(beta) * np.sqrt((v[t] ** 2).sum(1)) + np.sqrt((ut ** 2).sum(1))) * np.sqrt(k2)
         S = S + ut[:, :, None] * kt[:, None, :]
         o = scale * np.einsum("hij,hj->hi", S, qt)
         lim = u * np.abs(o) + 2.0 ** -25 + (scale * (1 + u) * eps * B * np.sqrt((qt * qt).sum(1)))[:, None]
@@ -249,3 +249,20 @@ def test_gdn_heads_that_write_little(K, T, dt, state, beta):  # noqa: F811
     for i in range(2 if state else 1):  # (with that scale the head that writes in full leaves the range)
         h, kh = slice(2 * i, 2 * i + 2), slice(i, i + 1)
         check_decaying(out[:, :, h], S1[:, h], q[:, :, kh], k[:, :, kh], v[:, :, h], gb[:, :, h], S[:, h], scale)
+
+
+@pytest.mark.parametrize("T", [8, 16, 90])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("power", [-6, -14, -60])
+def test_gdn_keys_of_any_size(K, T, dt, power):  # noqa: F811
+    """Keys far below norm 1 (fp16: with the bits that fp16 leaves them), alone and among keys of norm 1."""
+    q, k, v, gb, S = make_gdn(1, T, 2, 4, 128, dt, seed=23, sigma=0.0, g_scale=0.2)
+    k = k.clone()
+    k[:, :, 0] *= 2.0 ** power
+    k[:, ::3, 1] *= 2.0 ** power
+    scale = 2.0 ** (-power - 6) if dt == torch.bfloat16 else 1.0
+    for i in range(2):
+        h, kh = slice(2 * i, 2 * i + 2), slice(i, i + 1)
+        qi, ki, vi, gi, Si = q[:, :, kh], k[:, :, kh], v[:, :, h], gb[:, :, h].contiguous(), S[:, h].contiguous()
+        out, S1 = run_gdn(K, qi, ki, vi, gi, Si, scale=scale if i == 0 else 1.0)
+        check_decaying(out, S1, qi, ki, vi, gi, Si, scale if i == 0 else 1.0)
