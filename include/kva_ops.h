@@ -126,8 +126,8 @@ int kva_op_gdn_scan(const void* k, const void* v, const float* gb, float* state,
  * token in fp32 too (right, but about 10 times slower) if a g of it is above 0, a beta outside 0..1, a key's
  * norm above 1 by more than its rounding or (KVA_BF16) below 2^-6 but not 0, or a v not finite, or if a row of
  * the state decays in it by more than 256 to below that and its values' size.  Any finite state and v work.
- * A NaN or an infinity in v reaches its own column from its token on; one in a token's q or k or in its
- * gates can reach the tokens of its run before it too.
+ * A NaN or an infinity reaches what the recurrence takes it to: in v its own column from its token on, in k
+ * and the gates the heads that read them from their token on, in q its token's readouts.
  */
 typedef struct kva_gdn_forward_args {
   int32_t dtype;          /* 16-bit format of q, k, v and out: KVA_BF16 or KVA_F16 */

@@ -266,3 +266,27 @@ def test_gdn_keys_of_any_size(K, T, dt, power):  # noqa: F811
         qi, ki, vi, gi, Si = q[:, :, kh], k[:, :, kh], v[:, :, h], gb[:, :, h].contiguous(), S[:, h].contiguous()
         out, S1 = run_gdn(K, qi, ki, vi, gi, Si, scale=scale if i == 0 else 1.0)
         check_decaying(out, S1, qi, ki, vi, gi, Si, scale if i == 0 else 1.0)
+
+
+@pytest.mark.parametrize("T", [8, 16, 80])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_gdn_what_is_not_finite_reaches_no_token_before_it(K, T, dt, bad):  # noqa: F811
+    """In q: its token's readouts only; in k, g or beta: from its token on, in the heads that read it."""
+    q, k, v, gb, S = make_gdn(1, T, 2, 4, 128, dt, seed=24, g_scale=0.2)
+    out, S1 = run_gdn(K, q, k, v, gb, S)
+    t = T // 2 + 2
+    others = torch.arange(T, device="cuda") != t
+    q2 = q.clone()
+    q2[0, t, 0, 9] = bad
+    out2, S2 = run_gdn(K, q2, k, v, gb, S)
+    assert torch.equal(S2, S1) and torch.equal(out2[:, others], out[:, others])
+    assert torch.equal(out2[0, t, 2:], out[0, t, 2:]) and not torch.isfinite(out2[0, t, :2]).any()
+    k2, g2, b2 = k.clone(), gb.clone(), gb.clone()
+    k2[0, t, 0, 9], g2[0, 0, :2, t], b2[0, 1, :2, t] = bad, bad, bad
+    for ki, gi in ((k2, gb), (k, g2), (k, b2)):
+        out2, S2 = run_gdn(K, q, ki, v, gi, S)
+        assert torch.equal(S2[:, 2:], S1[:, 2:]) and torch.equal(out2[:, :, 2:], out[:, :, 2:])
+        assert not torch.isfinite(S2[:, :2]).all() and not torch.isfinite(out2[0, t, :2]).all()
+        check_decaying(out2[:, :t, :2], run_gdn(K, q[:, :t], k[:, :t], v[:, :t], gb[..., :t].contiguous(), S)[1][:, :2],
+                       q[:, :t, :1], k[:, :t, :1], v[:, :t, :2], gb[:, :, :2, :t], S[:, :2])
