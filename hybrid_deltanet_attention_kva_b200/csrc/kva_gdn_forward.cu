@@ -27,7 +27,8 @@ struct GdnFwd {
   int* err;
   int stall_run1;                  // test of the failure path: this run (from 1) is never handed over; 0: none
   int32_t lens[KVA_GDN_MAX_SEQ];
-  uint8_t order[KVA_GDN_MAX_SEQ];  // with lens, in runs: the sequences, longest first
+  uint8_t order[KVA_GDN_MAX_SEQ];  // with lens: the sequences, longest first
+  int first;                       // with lens: of those, the launch's first
 };
 static_assert(KVA_GDN_MAX_SEQ <= 256, "a sequence's number takes a byte");
 
@@ -84,8 +85,8 @@ __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constan
   __shared__ __align__(16) T ks[kStepTokens * D], qs[kStepTokens * D], vs[kStepTokens * ROWS];
   __shared__ float ds[kStepTokens], bs[kStepTokens];
   griddep_wait_and_release();
-  const int tid = threadIdx.x, h = blockIdx.x / PARTS, seq = blockIdx.y, r0 = (blockIdx.x % PARTS) * ROWS;
-  const int row = tid >> 3, l = tid & 7;
+  const int tid = threadIdx.x, h = blockIdx.x / PARTS, r0 = (blockIdx.x % PARTS) * ROWS;
+  const int seq = p.has_lens ? p.order[p.first + blockIdx.y] : blockIdx.y, row = tid >> 3, l = tid & 7;
   const int kh = h / (p.n_v / p.n_k);
   const int len = p.has_lens ? p.lens[seq] : p.T;
   const int64_t srow = ((static_cast<int64_t>(seq) * p.n_v + h) * D + r0 + row) * D + 4 * l;
@@ -912,7 +913,7 @@ __global__ void __launch_bounds__(32 * (ROWS / 16 + PREP), BLOCKS) gdn_chunk_ker
   }
   __syncthreads();
   griddep_wait_and_release();
-  const int seq = p.has_lens ? p.order[blockIdx.y] : blockIdx.y;
+  const int seq = p.has_lens ? p.order[p.first + blockIdx.y] : blockIdx.y;
   const int len = p.has_lens ? p.lens[seq] : p.T;
   if (warp < CHAIN) chain_runs<T, D, ROWS, PREP>(p, sm, h, half, seq, len, warp, lane, abort_flag);
   else prepare_runs<T, D, ROWS, PREP>(p, sm, h, half, seq, len, warp - CHAIN, lane, abort_flag);
@@ -928,16 +929,17 @@ cudaError_t launch_chunk(const GdnFwd& p, int n_seq, cudaStream_t s) {
 }
 
 template <typename T, int D>
-cudaError_t launch(const GdnFwd& p, int n_seq, int longest, cudaStream_t s) {
+cudaError_t launch_steps(const GdnFwd& p, int n_seq, cudaStream_t s) {
+  // two rows a thread where that still leaves four blocks an SM (64 sequences, 8 tokens: 117 us against 139
+  // with one row)
+  if (static_cast<int64_t>(p.n_v) * (D / 64) * n_seq >= 4 * num_sms())
+    return launch_pdl(gdn_recurrent_kernel<T, D, 2>, dim3(p.n_v * (D / 64), n_seq), dim3(256), 0, s, p);
+  return launch_pdl(gdn_recurrent_kernel<T, D, 1>, dim3(p.n_v * (D / 32), n_seq), dim3(256), 0, s, p);
+}
+template <typename T, int D>
+cudaError_t launch_runs(const GdnFwd& p, int n_seq, cudaStream_t s) {
   const int sms = num_sms();
   const int64_t blocks = static_cast<int64_t>(p.n_v) * (D / 64) * n_seq;  // of 64 state rows
-  if (longest <= kStepTokens) {
-    // two rows a thread where that still leaves four blocks an SM (64 sequences, 8 tokens: 117 us against 139
-    // with one row)
-    if (blocks >= 4 * sms)
-      return launch_pdl(gdn_recurrent_kernel<T, D, 2>, dim3(p.n_v * (D / 64), n_seq), dim3(256), 0, s, p);
-    return launch_pdl(gdn_recurrent_kernel<T, D, 1>, dim3(p.n_v * (D / 32), n_seq), dim3(256), 0, s, p);
-  }
   // A block that has its SM to itself takes a preparing warp on every scheduler (68 against 82 us for one
   // sequence of 1024 tokens).  With more work a head's 128 rows share one preparation, 6 to 9 % faster (8
   // sequences, bf16: 358 against 381 us) but for a last round that fills less than half of the SMs: there two
@@ -948,6 +950,18 @@ cudaError_t launch(const GdnFwd& p, int n_seq, int longest, cudaStream_t s) {
     if (last == 0 || 2 * last >= sms) return launch_chunk<T, D, 128, 4, 1>(p, n_seq, s);
   }
   return launch_chunk<T, D, 64, 2, 2>(p, n_seq, s);
+}
+// A sequence goes by its own length, whatever the others': the first n_long of the order in runs, the n_short
+// behind them token by token
+template <typename T, int D>
+cudaError_t launch(GdnFwd& p, int n_long, int n_short, cudaStream_t s) {
+  p.first = 0;
+  if (n_long > 0) {
+    const cudaError_t e = launch_runs<T, D>(p, n_long, s);
+    if (e != cudaSuccess || n_short == 0) return e;
+    p.first = n_long;
+  }
+  return launch_steps<T, D>(p, n_short, s);
 }
 
 bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -981,21 +995,20 @@ static int gdn_forward(const kva_gdn_forward_args* a, int32_t* err, void* stream
   if (!a16(a->state_in) || !a16(a->state_out)) return KVA_ERR_ALIGNMENT;
   GdnFwd p;
   p.has_lens = a->lens != nullptr;
-  int longest = a->T;
+  int n_long = a->T > kStepTokens ? a->n_seq : 0;
   if (a->lens) {
-    longest = 0;
+    n_long = 0;
     for (int i = 0; i < a->n_seq; ++i) {
       if (a->lens[i] < 0 || a->lens[i] > a->T) return KVA_ERR_INVALID_ARG;
       p.lens[i] = a->lens[i];
-      if (a->lens[i] > longest) longest = a->lens[i];
+      p.order[i] = static_cast<uint8_t>(i);
+      n_long += a->lens[i] > kStepTokens;
     }
     // the blocks of long sequences start first, so that the last ones to start are short (bf16, 16/48 heads:
     // 8 sequences of 1 to 1024 tokens 206 to 161 us, 16 of them 276 to 258, 32 of 1 to 512 409 to 379; 128 of 1
     // to 64 411 to 419)
-    if (longest > kStepTokens) {
-      for (int i = 0; i < a->n_seq; ++i) p.order[i] = static_cast<uint8_t>(i);
+    if (n_long > 0)
       std::stable_sort(p.order, p.order + a->n_seq, [&](int x, int y) { return p.lens[x] > p.lens[y]; });
-    }
   }
   p.q = a->q;
   p.k = a->k;
@@ -1021,10 +1034,10 @@ static int gdn_forward(const kva_gdn_forward_args* a, int32_t* err, void* stream
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f16 = a->dtype == KVA_F16;
   const cudaError_t r = a->d == 128
-                            ? (f16 ? launch<__half, 128>(p, a->n_seq, longest, s)
-                                   : launch<__nv_bfloat16, 128>(p, a->n_seq, longest, s))
-                            : (f16 ? launch<__half, 64>(p, a->n_seq, longest, s)
-                                   : launch<__nv_bfloat16, 64>(p, a->n_seq, longest, s));
+                            ? (f16 ? launch<__half, 128>(p, n_long, a->n_seq - n_long, s)
+                                   : launch<__nv_bfloat16, 128>(p, n_long, a->n_seq - n_long, s))
+                            : (f16 ? launch<__half, 64>(p, n_long, a->n_seq - n_long, s)
+                                   : launch<__nv_bfloat16, 64>(p, n_long, a->n_seq - n_long, s));
   return r == cudaSuccess ? KVA_OK : KVA_ERR_CUDA;
 }
 

@@ -119,8 +119,8 @@ int kva_op_gdn_scan(const void* k, const void* v, const float* gb, float* state,
  *   S_t = e^(g_t) S_(t-1) + u_t k_t^T          (= the recurrence of kva_op_gdn_scan)
  *   o_t = scale * S_t q_t
  * v head h reads k and q head h / (n_v / n_k).  The state is held in fp32 throughout.
- * Up to 8 tokens run one after the other in fp32; longer sequences in runs of 16 on the tensor
- * cores, where fp32 operands enter as the sum of two fp16 values (an error of 2^-21 relative), each row
+ * A sequence of up to 8 tokens runs token by token in fp32, a longer one in runs of 16 on the tensor
+ * cores (each by its own length), where fp32 operands enter as the sum of two fp16 values (an error of 2^-21 relative), each row
  * of the state's in units of a power of two that follows its data; what is below 2^-32 of the largest beta v
  * that a run brings the row and of the row as the run's first token meets it is dropped.  A run goes token by
  * token in fp32 too (right, but about 10 times slower) if a g of it is above 0, a beta outside 0..1, a key's

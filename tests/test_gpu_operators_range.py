@@ -290,3 +290,23 @@ def test_gdn_what_is_not_finite_reaches_no_token_before_it(K, T, dt, bad):  # no
         assert not torch.isfinite(S2[:, :2]).all() and not torch.isfinite(out2[0, t, :2]).all()
         check_decaying(out2[:, :t, :2], run_gdn(K, q[:, :t], k[:, :t], v[:, :t], gb[..., :t].contiguous(), S)[1][:, :2],
                        q[:, :t, :1], k[:, :t, :1], v[:, :t, :2], gb[:, :, :2, :t], S[:, :2])
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("lens", [[1, 100], [0, 8, 9, 1, 40, 8], [3, 17] * 9])
+def test_gdn_a_sequence_goes_by_its_own_length(K, dt, lens):  # noqa: F811
+    """Single and drafted tokens next to prompts in one call: each short sequence has every bit of a call of its
+    own, in place too, and nothing behind it is read or written."""
+    n, T = len(lens), max(lens)
+    q, k, v, gb, S = make_gdn(n, T, 2, 4, 128, dt, seed=25)
+    out, S1 = run_gdn(K, q, k, v, gb, S, lens=lens)
+    check_gdn(out, S1, q, k, v, gb, S, lens)
+    S2, out2 = S.clone(), torch.full_like(out, float("nan"))
+    K.kva_op_gdn_forward(q, k, v, gb, S2, S2, out2, lens=lens)
+    assert torch.equal(S2, S1)
+    for i, m in enumerate(lens):
+        assert torch.equal(out2[i, :m], out[i, :m]) and torch.isnan(out[i, m:]).all() and torch.isnan(out2[i, m:]).all()
+        if m <= 8:
+            a = [x[i:i + 1, :m] for x in (q, k, v)]
+            o, s = run_gdn(K, *a, gb[i:i + 1, :, :, :m].contiguous(), S[i:i + 1])
+            assert torch.equal(o[0], out[i, :m]) and torch.equal(s[0], S1[i])
