@@ -46,6 +46,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
+__device__ __forceinline__ float reciprocal(float x) {  // of the largest x too, which is subnormal
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // One q8_0 code in the low byte, y inv to the nearest integer, in one instruction and without the
 // conversion unit: in the sum with 1.5 x 2^23 a last place is 1, and its low byte is the code in two's
 // complement.
@@ -123,10 +128,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
       if (i < n) {
         const bool fine = amax < __int_as_float(0x7f800000);
         const float d = amax * (1.f / 127.f);
-        // 127 / max to the last place, and one up, so that a half goes away from zero; what is nearer to a
-        // half than 127 x 2^-22 may too.  (From a subnormal d the reciprocal could overflow; such a d is 0 in
-        // fp16, whatever the codes.)
-        const float r = __fdividef(1.f, amax), near = 127.f * r;
+        // 127 / max to the last place by one Newton step (the residual 127 - max near, times the reciprocal), and
+        // one up, so that a half goes away from zero; what is nearer to a half than 127 x 2^-22 may too.  (From
+        // a subnormal d the reciprocal could overflow; such a d is 0 in fp16, whatever the codes.)
+        const float r = reciprocal(amax), near = 127.f * r;
         const float up = __uint_as_float(__float_as_uint(fmaf(fmaf(-amax, near, 127.f), r, near)) + 1);
         const float inv = fine && d >= 1.1754944e-38f ? up : 0.f;
         uint32_t c = 0;

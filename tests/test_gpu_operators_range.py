@@ -310,3 +310,60 @@ def test_gdn_a_sequence_goes_by_its_own_length(K, dt, lens):  # noqa: F811
             a = [x[i:i + 1, :m] for x in (q, k, v)]
             o, s = run_gdn(K, *a, gb[i:i + 1, :, :, :m].contiguous(), S[i:i + 1])
             assert torch.equal(o[0], out[i, :m]) and torch.equal(s[0], S1[i])
+
+
+# ------------------------------------------------------------------ residual add + RMSNorm, q8_0 codes
+def q8_of(K, g):  # noqa: F811
+    """Codes and scales of rows whose normalised values are +g and -g: a row of ones has the norm 1, which
+    leaves every bit of g."""
+    n = g.numel()
+    h = torch.ones(2, n, device="cuda")
+    h[1] = -1
+    x, ho = torch.zeros_like(h), torch.empty_like(h)
+    codes, sc = torch.empty(2, n, dtype=torch.int8, device="cuda"), torch.empty(n // 32, 2, dtype=torch.float16, device="cuda")
+    K.kva_op_add_rmsnorm(x, h, g, ho, codes, scales=sc, eps=0.0)
+    return f64(codes), f64(sc)
+
+
+def test_add_rmsnorm_q8_codes_are_the_nearest(K):  # noqa: F811
+    """y / d with d = max|y| / 127, to the nearest, halves away from zero.  The kernel's reciprocal is off by at
+    most 1.5 last places and its product by half of one, 127 x 2^-22 of a code together: nearer to a half
+    than that, and only there, either neighbour stands.  Exact halves (max|y| a power of two times 127) go away from
+    zero."""
+    rng = np.random.default_rng(5)
+    blocks = 512
+    big = (rng.uniform(1, 2, blocks) * 2.0 ** rng.integers(-20, 12, blocks)).astype(np.float32)
+    big[:32] = 127 * 2.0 ** rng.integers(-20, 12, 32)
+    half = (rng.integers(-127, 127, (blocks, 32)) + 0.5) * big[:, None].astype(np.float64) / 127
+    y = half.astype(np.float32)
+    for step in range(1, 5):  # the floats on both sides of a half
+        y[:, step] = np.nextafter(y[:, step], np.float32(np.inf))
+        y[:, 4 + step] = np.nextafter(y[:, 4 + step], np.float32(-np.inf))
+    y[:, 9:20] = (rng.uniform(-1, 1, (blocks, 11)) * big[:, None]).astype(np.float32)
+    y[32:, 20:31] *= (1 + rng.uniform(-1e-4, 1e-4, (blocks - 32, 11))).astype(np.float32)
+    y[:, 31] = big * np.where(rng.random(blocks) < 0.5, 1, -1)
+    y = np.clip(y, -big[:, None], big[:, None])
+    codes, sc = q8_of(K, torch.from_numpy(y.reshape(-1)).cuda())
+    for r, sign in ((0, 1), (1, -1)):
+        q = sign * y.astype(np.float64) * 127 / big[:, None].astype(np.float64)
+        want = np.sign(q) * np.floor(np.abs(q) + 0.5)
+        got = codes[r].reshape(blocks, 32)
+        near = np.abs(np.abs(q) % 1 - 0.5) <= 127 * 2.0 ** -22
+        assert (np.abs(got - q) <= 0.5 + 127 * 2.0 ** -22).all()
+        assert np.array_equal(got[~near], want[~near]) and near.sum() < near.size / 2
+        exact = np.abs(q) % 1 == 0.5
+        assert np.array_equal(got[exact], want[exact]) and exact.sum() > 300
+        d = (big.astype(np.float64) / 127)
+        assert (np.abs(sc[:, r] - d) <= d * (2.0 ** -11 + 2.0 ** -23) + 2.0 ** -25).all()
+
+
+def test_add_rmsnorm_q8_codes_of_the_largest_and_smallest_blocks(K):  # noqa: F811
+    """Up to fp32's largest value: the codes stand, the scale is infinite where fp16 ends.  Blocks below fp16's
+    scales have the scale 0."""
+    tops = [2.0 ** 20, 2.0 ** 100, 2.0 ** 125, 2.0 ** 126, 1.5 * 2.0 ** 126, 2.0 ** 127, 3.4e38, 2.0 ** -40, 2.0 ** -118]
+    y = torch.linspace(-1, 1, 32, dtype=torch.float64)[None] * torch.tensor(tops, dtype=torch.float64)[:, None]
+    codes, sc = q8_of(K, y.float().reshape(-1).cuda())
+    q = y.float().double() * 127 / y.float().double().abs().amax(1, keepdim=True)
+    assert np.array_equal(codes[0].reshape(-1, 32), f64(torch.round(q))) and np.array_equal(codes[1], -codes[0])
+    assert np.isfinite(sc[0]).all() and (sc[1:7] == np.inf).all()
+    assert (sc[7:] == 0).all()
