@@ -41,11 +41,6 @@ struct Io<__half> : Io16<__half> {};
 template <>
 struct Io<__nv_bfloat16> : Io16<__nv_bfloat16> {};
 
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
 __device__ __forceinline__ float reciprocal(float x) {  // of the largest x too, which is subnormal
   float y;
   asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -37,31 +37,6 @@ static_assert(KVA_GDN_MAX_SEQ <= 256, "a sequence's number takes a byte");
 // for 64; a token more costs 0.5 us, 2.5 us and 11 us, a run nothing until it is full.
 constexpr int kStepTokens = 8;
 
-// two fp32 operations an instruction
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-  return d;
-}
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) {  // a - b: b times -1 is exact
-  float2 d, m1 = make_float2(-1.f, -1.f);
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(b)), "l"(reinterpret_cast<unsigned long long&>(m1)),
-        "l"(reinterpret_cast<unsigned long long&>(a)));
-  return d;
-}
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
-        "l"(reinterpret_cast<unsigned long long&>(c)));
-  return d;
-}
 __device__ __forceinline__ float sum4(float v) {  // over the 4 lanes of a fragment's row
   v += __shfl_xor_sync(0xffffffffu, v, 2);
   v += __shfl_xor_sync(0xffffffffu, v, 1);

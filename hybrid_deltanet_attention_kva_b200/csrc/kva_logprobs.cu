@@ -44,28 +44,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-
-// two fp32 operations an instruction
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
-        "l"(reinterpret_cast<unsigned long long&>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-  return d;
-}
 
 // 16 bytes of logits
 template <typename T>
@@ -136,7 +114,6 @@ struct Sums {
     l = LOG2E;
     s = w = make_float2(0.f, 0.f);
   }
-  __device__ __forceinline__ bool huge() const { return l != LOG2E; }
   __device__ __forceinline__ void rebase(float to) {
     const float ln = fabsf(to) > 1e38f ? 1.f : LOG2E, rn = to * ln;
     const float d = l == LOG2E && ln == LOG2E ? fmaxf(r - rn, T_MIN) : T_MIN, f = ex2(d);
