@@ -159,7 +159,7 @@ struct Args {
 template <typename TX, typename TH, typename TO, int TPR, int NV>
 cudaError_t launch(const Args& a) {
   constexpr int THREADS = TPR < 256 ? 256 : TPR, RPB = THREADS / TPR;
-  return launch_pdl(add_rmsnorm_kernel<TX, TH, TO, TPR, NV>, dim3((a.rows + RPB - 1) / RPB), dim3(THREADS), 0, a.s,
+  return launch_pdl(add_rmsnorm_kernel<TX, TH, TO, TPR, NV>, dim3((static_cast<unsigned>(a.rows) + RPB - 1) / RPB), dim3(THREADS), 0, a.s,
                     static_cast<const TX*>(a.x), a.ldx, static_cast<const TH*>(a.h), static_cast<TH*>(a.h_out), a.ldh,
                     a.g, static_cast<TO*>(a.out), a.ldo, static_cast<__half*>(a.scales), a.rows, a.n, a.eps);
 }

@@ -367,3 +367,18 @@ def test_add_rmsnorm_q8_codes_of_the_largest_and_smallest_blocks(K):  # noqa: F8
     assert np.array_equal(codes[0].reshape(-1, 32), f64(torch.round(q))) and np.array_equal(codes[1], -codes[0])
     assert np.isfinite(sc[0]).all() and (sc[1:7] == np.inf).all()
     assert (sc[7:] == 0).all()
+
+
+def test_add_rmsnorm_as_many_rows_as_an_int32_counts(K):  # noqa: F811
+    """2^31 - 1 rows of 4 (17 GB a tensor)."""
+    rows = 2 ** 31 - 1
+    x = torch.zeros(rows, 4, dtype=torch.float16, device="cuda")
+    h = torch.ones_like(x)
+    h[-3:] *= torch.tensor([[2.0], [-1.0], [0.0]], device="cuda", dtype=torch.float16)
+    g = torch.tensor([1.0, 2.0, 3.0, 4.0], device="cuda")
+    out = torch.empty_like(x)
+    K.kva_op_add_rmsnorm(x, h, g, h, out, eps=0.0)
+    want = torch.tensor([1.0, 2.0, 3.0, 4.0], device="cuda", dtype=torch.float16)
+    for part in out[:-3].split(2 ** 28):
+        assert (part == want).all()
+    assert torch.equal(out[-3], want) and torch.equal(out[-2], -want) and torch.isnan(out[-1]).all()
