@@ -489,6 +489,12 @@ def _dense(t: Optional[torch.Tensor], shape: tuple, dtype, what: str) -> Optiona
     return t.data_ptr()
 
 
+def _fits_int32(*sizes) -> None:
+    """The C entries take int32 sizes, to which ctypes would cut larger ones."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"a size of {max(sizes)} is above 2^31 - 1")
+
+
 def _row_stride(t: torch.Tensor, shape, what: str) -> int:
     """Row stride of a 2-D tensor of this shape whose rows are contiguous (over a single row it is
     never used: the row's length)."""
@@ -518,6 +524,7 @@ def _gdn_forward(entry: str, q, k, v, gb, state_in, state_out, out, lens, scale,
     v_shape = (n_seq, T, v.shape[2], d)
     n_v = v_shape[2]
     dev, s = _one_device(stream, q, k, v, gb, state_in, state_out, out, err)
+    _fits_int32(n_seq, T, n_k, n_v)
     strides = []
     for name, t, shape in (("q", q, qk_shape), ("k", k, qk_shape), ("v", v, v_shape), ("out", out, v_shape)):
         if t.dtype != dt or t.shape != shape:
@@ -558,6 +565,7 @@ def kva_op_add_rmsnorm(x: torch.Tensor, h: torch.Tensor, g: torch.Tensor, h_out:
     shape = x.shape
     rows, n = shape
     dev, s = _one_device(stream, x, h, g, h_out, out, scales)
+    _fits_int32(rows, n)
     if h_out.dtype != h.dtype:
         raise ValueError("h and h_out must have one dtype")
     ldx, ldh = _row_stride(x, shape, "x"), _row_stride(h, shape, "h")
@@ -584,6 +592,7 @@ def kva_op_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] =
     rows, V = logits.shape
     one, f32, i32 = (rows,), torch.float32, torch.int32
     dev, s = _one_device(stream, logits, tokens, logprob, lse, entropy, top_id, top_logprob)
+    _fits_int32(rows, V)
     ld = _row_stride(logits, (rows, V), "logits")
     n_top = 0 if top_id is None else top_id.shape[-1]
     if (top_id is None) != (top_logprob is None) or (tokens is None) != (logprob is None):

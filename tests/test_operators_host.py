@@ -136,6 +136,30 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(monkeypatch):
             K.kva_op_token_logprobs(x, **bad)
 
 
+def test_binding_refuses_sizes_above_int32(monkeypatch):
+    """The C entries take int32 sizes: 2^32 + 3 rows may not pass as 3.  (Tensors without memory; nothing
+    may reach the library.)"""
+    monkeypatch.setattr(kmod, "_one_device", lambda *a: (0, 0))
+
+    def reached(*a):
+        raise AssertionError("reached the library")
+    monkeypatch.setattr(kmod, "_call_on", reached)
+    big, e = 2 ** 32 + 3, torch.empty
+    f16, f32 = dict(dtype=torch.float16, device="meta"), dict(dtype=torch.float32, device="meta")
+    for rows, n in ((big, 4), (1, big)):
+        with pytest.raises(ValueError, match="above"):
+            K.kva_op_add_rmsnorm(e(rows, n, **f16), e(rows, n, **f32), e(n, **f32), e(rows, n, **f32), e(rows, n, **f16))
+        with pytest.raises(ValueError, match="above"):
+            K.kva_op_token_logprobs(e(rows, n, **f16), lse=e(rows, **f32))
+    for T, nk, nv in ((big, 1, 1), (1, big, big), (1, 1, big)):
+        q, v, S = e(1, T, nk, 64, **f16), e(1, T, nv, 64, **f16), e(1, nv, 64, 64, **f32)
+        with pytest.raises(ValueError, match="above"):
+            K.kva_op_gdn_forward(q, q, v, e(1, 2, nv, T, **f32), S, S, v)
+    with pytest.raises(ValueError, match="sequences|above"):
+        q = e(big, 1, 1, 64, **f16)
+        K.kva_op_gdn_forward(q, q, q, e(big, 2, 1, 1, **f32), e(big, 1, 64, 64, **f32), e(big, 1, 64, 64, **f32), q)
+
+
 def test_argument_struct_and_limits_match_the_c_compiler(tmp_path):
     fields = [n for n, _ in K.KvaGdnForwardArgs._fields_]
     src = ["#include <stdio.h>", "#include <stddef.h>", '#include "kva_ops.h"', "int main(void){",
