@@ -312,6 +312,23 @@ def test_gdn_a_sequence_goes_by_its_own_length(K, dt, lens):  # noqa: F811
             assert torch.equal(o[0], out[i, :m]) and torch.equal(s[0], S1[i])
 
 
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d,nv,n", [(128, 50, 7), (128, 24, 4), (64, 100, 3)])
+def test_gdn_a_sequence_has_the_same_bits_in_any_batch(K, dt, d, nv, n):  # noqa: F811
+    """Alone, beside others of its length, and beside others of other lengths, whatever layout of the work that
+    takes."""
+    T = 50
+    q, k, v, gb, S = make_gdn(n, T, 2, nv, d, dt, seed=26, g_scale=0.3)
+    out, S1 = run_gdn(K, q, k, v, gb, S)
+    lens = [T, 3, 30, 0, 20, 8, 9][:n]
+    out2, S2 = run_gdn(K, q, k, v, gb, S, lens=lens)
+    assert torch.equal(out2[0], out[0]) and torch.equal(S2[0], S1[0])
+    for i in (0, n - 1):
+        one = [x[i:i + 1] for x in (q, k, v, gb, S)]
+        o, s = run_gdn(K, *one)
+        assert torch.equal(o[0], out[i]) and torch.equal(s[0], S1[i])
+
+
 # ------------------------------------------------------------------ residual add + RMSNorm, q8_0 codes
 def q8_of(K, g):  # noqa: F811
     """Codes and scales of rows whose normalised values are +g and -g: a row of ones has the norm 1, which
