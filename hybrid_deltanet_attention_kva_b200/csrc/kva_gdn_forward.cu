@@ -32,9 +32,10 @@ struct GdnFwd {
 };
 static_assert(KVA_GDN_MAX_SEQ <= 256, "a sequence's number takes a byte");
 
-// Sequences of at most this many tokens go token by token, longer ones in runs of 16: at 8 tokens of a
-// 16/48-head layer 5.7 us against 5.1 for one sequence, but 33 against 38 for 16 and 117 against 133
-// for 64; a token more costs 0.5 us, 2.5 us and 11 us, a run nothing until it is full.
+// Sequences of at most this many tokens go token by token, longer ones in runs of 16.  At 8 tokens of a
+// 16/48-head layer (bf16) one sequence takes 6.0 us against 6.9 in a run, 16 take 33.5 against 50.6, 64 take 115
+// against 171 (fp16: 5.9 against 5.9, one sequence); a token more costs 0.4 us, 3 us and 11 us, a run nothing until
+// it is full.  One number, so that a sequence's result does not depend on its neighbours.
 constexpr int kStepTokens = 8;
 
 __device__ __forceinline__ float sum4(float v) {  // over the 4 lanes of a fragment's row
@@ -161,16 +162,20 @@ __global__ void __launch_bounds__(256) gdn_recurrent_kernel(const __grid_constan
 // The state may not see a 16-bit rounding (it carries over thousands of tokens), so S, W, Tm and the
 // updates enter as two fp16 terms: two products where the partner is K or Q, three where it has two terms
 // itself.  So do S and M on the way to the readout, which sees one 16-bit rounding only, the output's.  That
-// makes 110 MMAs a warp and run.  The terms are in units that follow the data, or small states and values would
+// makes 108 MMAs a warp and run.  The terms are in units that follow the data, or small states and values would
 // lose fp16's last bits (1e-3 of a state of 1e-4) and large ones leave its range; bf16 inputs take fp16 terms as
 // well: two bf16 terms left states 3.4e-6 off after 1024 tokens (fp16 terms: 2e-7), three of them would cost
 // 30 % of the time.
 //
 // What bounds it: a run's chain of dependent steps.  16/48 heads of 128, one sequence of 1024
-// tokens (96 blocks, one chain warp a scheduler): fp16 66 us, 1.03 us a run, of which Y and Z 945 cycles, W
-// and U 310, the state's update 390, O and its stores 365 (bf16 74 us); eight sequences, where two chain
-// warps share a scheduler: fp16 301 us, bf16 with its units 357 us.  Measured and not kept (us for 1 / 8
-// sequences, against the state of that step): runs of 32 tokens (100 / 399 against 82 / 362), the columns
+// tokens (96 blocks, one chain warp a scheduler): fp16 84 us, 1.3 us a run, bf16 89 us; eight sequences, where
+// two chain warps share a scheduler: fp16 385 us, bf16 400 us (tensor pipe 47 % and issue slots 51 % busy).
+// Left out one at a time in a copy, the state's second term on the way to the readout costs 6 us of the 84
+// (27 to 36 us of eight sequences), the second terms of M and of the updates there 2, the units 1.
+// Measured and not kept (us for 1 / 8 sequences, against the state of that step): the state's update added to it
+// behind the products, so that they do not cut its last bit (states after 1024 tokens without decay 4.8e-7 off
+// instead of 1.1e-6; 84 / 435 against 84 / 385, fp16), keys in units of their own (84 / 439 against 84 / 396, bf16),
+// runs of 32 tokens (100 / 399 against 82 / 362), the columns
 // split over pairs of warps (76 / 450 against 68 / 349), the update fused with the next run's Y (75 / 380
 // against 68 / 349), readouts by warps of their own (69 / 363 against 66 / 349), Tm diag(e^gam) K formed by the
 // preparing warps, so that U is V^T Tm^T less a product with S (78 / 387 against 66 / 357: the second term's
@@ -606,7 +611,8 @@ __device__ void prepare_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int 
 
 // n tokens from t0 on, one after the other in fp32, for the rows of a chain warp: a run that fp16 terms in one
 // unit cannot hold.  `state`: a lane's fragments of S in true size; `row`: its first row of the head.  (Out of
-// line, as between the runs' steps its instructions cost them 6 %: 8 sequences 412 against 394 us.)
+// line, as between the runs' steps its instructions cost them 1 to 2 %: 16 sequences 814 against 799 us.)  A run
+// takes about ten times as long this way: a sequence of 1024 tokens 0.93 ms, eight 3.6 ms.
 template <typename T, int D>
 __device__ __noinline__ void step_tokens(const GdnFwd& p, float* state, int h, int row, int seq, int t0, int n,
                                          int lane) {
@@ -729,7 +735,8 @@ __device__ void chain_runs(const GdnFwd& p, uint8_t* sm, int h, int half, int se
         mma2(z[0], z[1], al, qf[ks & 1], 0, 2, 1, 3);
       }
       // Units for the run, from its values and the state's rows as its tokens meet them.  (The test comes after
-      // the products, which hide what it waits for: before them 421 against 406 us for 8 sequences.)
+      // the products, which hide what it waits for: fp16, 8 sequences, 385 against 392 us with it before them; bf16
+      // 400 against 394.)
       const T* vm = reinterpret_cast<const T*>(st + St::VM) + warp * 16 + gr;
       const float2 mv = make_float2(F16<T>::to(vm[0]), F16<T>::to(vm[8]));
       const float most = fmaxf(gv.w, 0x1p-100f);  // (a smaller beta is written with fewer bits)
@@ -905,7 +912,7 @@ cudaError_t launch_chunk(const GdnFwd& p, int n_seq, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t launch_steps(const GdnFwd& p, int n_seq, cudaStream_t s) {
-  // two rows a thread where that still leaves four blocks an SM (64 sequences, 8 tokens: 117 us against 139
+  // two rows a thread where that still leaves four blocks an SM (64 sequences, 8 tokens: 115 us against 139
   // with one row)
   if (static_cast<int64_t>(p.n_v) * (D / 64) * n_seq >= 4 * num_sms())
     return launch_pdl(gdn_recurrent_kernel<T, D, 2>, dim3(p.n_v * (D / 64), n_seq), dim3(256), 0, s, p);
@@ -915,10 +922,10 @@ template <typename T, int D>
 cudaError_t launch_runs(const GdnFwd& p, int n_seq, cudaStream_t s) {
   const int sms = num_sms();
   const int64_t blocks = static_cast<int64_t>(p.n_v) * (D / 64) * n_seq;  // of 64 state rows
-  // A block that has its SM to itself takes a preparing warp on every scheduler (68 against 82 us for one
-  // sequence of 1024 tokens).  With more work a head's 128 rows share one preparation, 6 to 9 % faster (8
-  // sequences, bf16: 358 against 381 us) but for a last round that fills less than half of the SMs: there two
-  // blocks of 64 rows an SM end sooner (4 sequences: 220 against 239 us).
+  // A block that has its SM to itself takes a preparing warp on every scheduler (one sequence of 1024 tokens: fp16
+  // 84 against 90 us, bf16 89 against 98).  With more work a head's 128 rows share one preparation (8 sequences:
+  // fp16 385 against 407 us, bf16 400 against 442) but for a last round that fills less than half of the SMs: there
+  // two blocks of 64 rows an SM end sooner (4 sequences: 240 against 267 us; 16: 799 against 794).
   if (blocks <= sms) return launch_chunk<T, D, 64, 4, 1>(p, n_seq, s);
   if constexpr (D == 128) {
     const int64_t last = blocks / 2 % sms;
@@ -980,8 +987,8 @@ static int gdn_forward(const kva_gdn_forward_args* a, int32_t* err, void* stream
       n_long += a->lens[i] > kStepTokens;
     }
     // the blocks of long sequences start first, so that the last ones to start are short (bf16, 16/48 heads:
-    // 8 sequences of 1 to 1024 tokens 206 to 161 us, 16 of them 276 to 258, 32 of 1 to 512 409 to 379; 128 of 1
-    // to 64 411 to 419)
+    // 8 sequences of 1 to 1024 tokens 279 to 225 us, 16 of them 336 to 299, 32 of 1 to 512 505 to 482, 128 of 1 to 64
+    // 426 to 411)
     if (n_long > 0)
       std::stable_sort(p.order, p.order + a->n_seq, [&](int x, int y) { return p.lens[x] > p.lens[y]; });
   }
