@@ -174,7 +174,8 @@ int kva_test_gdn_forward_wait_timeout(const kva_gdn_forward_args* a, int32_t* er
  *     32 values d = max|y| / 127, codes round(y / d) half away from zero (either neighbour
  *     within 127 x 2^-22 of a half), d rounded to fp16 for storage (infinite above its range);
  *     a block that holds a NaN or an infinity gets the scale NaN and codes 0.
- * The sum of squares is fp32, as in kva_op_rmsnorm: |h_out| up to 2^56.
+ * The sum of squares is fp32, as in kva_op_rmsnorm: |h_out| up to 2^56 (and, with an eps of 0, the row's
+ * root mean square at least 2^-60).
  * n, ldx, ldh and ldo multiples of 4 (ldo of 16 bytes for q8_0), n <= 16384; pointers
  * 16-byte aligned (scales: 2). */
 int kva_op_add_rmsnorm(const void* x, int32_t x_dtype, int64_t ldx, const void* h, void* h_out,
