@@ -329,6 +329,41 @@ def test_gdn_a_sequence_has_the_same_bits_in_any_batch(K, dt, d, nv, n):  # noqa
         assert torch.equal(o[0], out[i]) and torch.equal(s[0], S1[i])
 
 
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+def test_gdn_mixed_calls_one_after_another_captured_and_replayed(K, dt):  # noqa: F811
+    """Prompts and single tokens (two launches a call), the state of one call going into the next, in place, with
+    runs that go token by token among them: a replayed graph and eager calls on another stream end alike."""
+    n, T, lens = 4, 60, [[1, 60, 8, 33], [40, 1, 0, 9], [3, 2, 60, 1]]
+    q, k, v, gb, S = make_gdn(n, T, 2, 6, 128, dt, seed=27)
+    gb[1, 0, 2, 20] = 0.5
+    out = torch.full((3, *v.shape), float("nan"), dtype=dt, device="cuda")
+
+    def calls(state, o, **kw):
+        for i, m in enumerate(lens):
+            K.kva_op_gdn_forward(q, k, v, gb, state, state, o[i], lens=m, **kw)
+
+    S1, side = S.clone(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    calls(S1, out, stream=side)
+    side.synchronize()
+    S2, out2 = S.clone(), torch.full_like(out, float("nan"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls(S2, out2)
+    for _ in range(3):
+        S2.copy_(S)
+        out2.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(S2, S1) and torch.equal(out2.nan_to_num(7.0), out.nan_to_num(7.0))
+    want = S
+    for i, m in enumerate(lens):
+        o, after = run_gdn(K, q, k, v, gb, want, lens=m)
+        assert torch.equal(o.nan_to_num(7.0), out[i].nan_to_num(7.0))
+        want = after
+    assert torch.equal(want, S1)
+
+
 # ------------------------------------------------------------------ residual add + RMSNorm, q8_0 codes
 def q8_of(K, g):  # noqa: F811
     """Codes and scales of rows whose normalised values are +g and -g: a row of ones has the norm 1, which
